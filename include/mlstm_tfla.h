@@ -528,6 +528,135 @@ int mlstm_bw_grads(const mlstm_fw_desc_t* desc,
                    void* workspace, size_t workspace_bytes,
                    void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated delta rule: the matrix memory above with sigmoid gates, where each
+ * step first subtracts what the memory already returns for its key.  Per
+ * head, with a_t = sigmoid(f_t), b_t = sigmoid(i_t), s = qk_scale:
+ *
+ *   u_t = b_t (v_t - a_t C_{t-1}^T k_t)
+ *   C_t = a_t C_{t-1} + k_t u_t^T        ( = a_t (I - b_t k_t k_t^T) C_{t-1}
+ *   h_t = s C_t^T q_t                          + b_t k_t v_t^T )
+ *
+ * There is no normaliser and no max-state.  The state stays bounded while
+ * b_t |k_t|^2 < 2: keys of unit length satisfy it, and the library does not
+ * scale them.  Tensors, layouts, alignment, streams and status codes are
+ * those of the conventions at the top of this file.  Gates may be infinite:
+ * f_t = -inf clears the memory before step t exactly (a document's end),
+ * f_t = +inf keeps all of it, i_t = -inf writes nothing, i_t = +inf has
+ * b_t = 1.  Other non-finite inputs spread as NaN.
+ *
+ * Arithmetic: every operand computed in float32 (the state, U, the inverse
+ * within a chunk) enters the bf16 matrix cores in three parts of eight bits,
+ * float32 inputs too; products accumulate in float32, the sums of log a
+ * within a chunk in double.  Terms of dQ and dK that are stored as bf16 use
+ * two parts where nothing else reads them. */
+typedef struct {
+  int32_t B, NH;       /* batch, heads: >= 1; B * NH * ceil(S / 32) and
+                          B * NH * DHV / 64 below 2^23                        */
+  int32_t S;           /* sequence length: 0 .. 2^30, any value               */
+  int32_t DHQK;        /* 64, 128 or 256                                      */
+  int32_t DHV;         /* multiple of 64, at most 512                         */
+  int32_t qkv_dtype;   /* mlstm_dtype_t of Q, K, V and of dQ, dK, dV          */
+  int32_t h_dtype;     /* mlstm_dtype_t of H and dH                           */
+  float qk_scale;      /* s; <= 0 selects 1/sqrt(DHQK)                        */
+  int32_t reserved[4]; /* must be zero                                        */
+} mlstm_delta_desc_t;
+
+/* Host-only check of a descriptor: MLSTM_OK or the first error found. */
+int mlstm_delta_validate(const mlstm_delta_desc_t* desc);
+
+/* Bytes of device workspace of mlstm_delta_fw and mlstm_delta_bw; 0 for an
+ * invalid descriptor.  Forward: two L x L float32 matrices and three decays a
+ * row for every chunk of L rows (64; 32 for float32 inputs).  Backward: also
+ * the state entering and the state gradient behind every chunk (DHQK x DHV
+ * float32 each), and U and dV in float32. */
+size_t mlstm_delta_fw_workspace_bytes(const mlstm_delta_desc_t* desc);
+size_t mlstm_delta_bw_workspace_bytes(const mlstm_delta_desc_t* desc);
+
+/* Forward pass.
+ *   C0        (B, NH, DHQK, DHV) float32, may be NULL: zero initial state.
+ *   H         (B, NH, S, DHV) h_dtype.
+ *   C_out     may be NULL: the final state is not written.
+ *   workspace at least mlstm_delta_fw_workspace_bytes(desc) bytes, 256-byte
+ *             aligned; may be NULL when that is 0.
+ * With S == 0 the call only writes C_out. */
+int mlstm_delta_fw(const mlstm_delta_desc_t* desc,
+                   const void* Q, const void* K, const void* V,
+                   const float* i_pre, const float* f_pre, const float* C0,
+                   void* H, float* C_out,
+                   void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Backward pass: the gradients of sum(dH * H) + sum(dC_out * C_out).
+ *   dH          (B, NH, S, DHV) h_dtype, 16-byte aligned, required.
+ *   dC_out      (B, NH, DHQK, DHV) float32, may be NULL: zero.
+ *   dQ, dK, dV  qkv_dtype, shapes of Q, K, V, 16-byte aligned, required.
+ *   d_i, d_f    (B, NH, S) float32, required.  A gate at an infinity that
+ *               closes it has gradient zero.
+ *   dC0         (B, NH, DHQK, DHV) float32, may be NULL.
+ *   workspace   at least mlstm_delta_bw_workspace_bytes(desc) bytes, 256-byte
+ *               aligned; may be NULL when that is 0.
+ * The forward quantities are formed again.  Equal inputs give equal bits.
+ * With S == 0 only dC0 is written (dC_out, or zeros). */
+int mlstm_delta_bw(const mlstm_delta_desc_t* desc,
+                   const void* Q, const void* K, const void* V,
+                   const float* i_pre, const float* f_pre, const float* C0,
+                   const void* dH, const float* dC_out,
+                   void* dQ, void* dK, void* dV, float* d_i, float* d_f, float* dC0,
+                   void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* One time step for every head (decode); S must be 1 (else MLSTM_E_SHAPE).
+ *   q, k (B, NH, DHQK), v (B, NH, DHV) qkv_dtype; i_pre, f_pre (B, NH) float32
+ *   C_in  (B, NH, DHQK, DHV) float32, 16-byte aligned, NULL = zero state
+ *   h     (B, NH, DHV) h_dtype, 16-byte aligned, required
+ *   C_out as C_in, required; it may be C_in itself (updated in place). */
+int mlstm_delta_step(const mlstm_delta_desc_t* desc,
+                     const void* q, const void* k, const void* v,
+                     const float* i_pre, const float* f_pre, const float* C_in,
+                     void* h, float* C_out,
+                     void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Head norm: the layer norm of every row of the cell's output over its D
+ * values, with a weight and a bias per head and channel,
+ *   y = (x - mean) / sqrt(var + eps) * weight + bias,
+ * from H's layout (B, NH, S, D) to (B, S, NH, D), the layout of the output
+ * projection.  Mean and variance (the mean of squares) in float32. */
+typedef struct {
+  int32_t B, NH;       /* >= 1                                                */
+  int32_t S;           /* >= 0                                                */
+  int32_t D;           /* multiple of 64, at most 512                         */
+  int32_t x_dtype;     /* mlstm_dtype_t of x and dx                           */
+  int32_t y_dtype;     /* mlstm_dtype_t of y and dy                           */
+  float eps;           /* >= 0, finite                                        */
+  int32_t reserved[3]; /* must be zero                                        */
+} mlstm_head_norm_desc_t;   /* B * NH * S < 2^26, NH < 2^22, B * S < 2^30 */
+
+int mlstm_head_norm_validate(const mlstm_head_norm_desc_t* desc);
+
+/* Bytes of device workspace of mlstm_head_norm_bw when dweight or dbias is
+ * asked for (partial sums); 0 for an invalid descriptor. */
+size_t mlstm_head_norm_bw_workspace_bytes(const mlstm_head_norm_desc_t* desc);
+
+/*   x       (B, NH, S, D) x_dtype, 16-byte aligned
+ *   weight, bias (NH, D) float32, 16-byte aligned, may be NULL (ones, zeros)
+ *   y       (B, S, NH, D) y_dtype, 16-byte aligned */
+int mlstm_head_norm_fw(const mlstm_head_norm_desc_t* desc,
+                       const void* x, const float* weight, const float* bias,
+                       void* y, void* stream);
+
+/* Gradients of sum(dy * y).  dx has the shape and type of x and may not alias
+ * it; dweight, dbias (NH, D) float32 may each be NULL (not written), and with
+ * both NULL no workspace is needed.  Mean and variance are formed again from
+ * x.  The sums over rows are taken in a fixed order: equal inputs give equal
+ * bits. */
+int mlstm_head_norm_bw(const mlstm_head_norm_desc_t* desc,
+                       const void* x, const float* weight, const void* dy,
+                       void* dx, float* dweight, float* dbias,
+                       void* workspace, size_t workspace_bytes,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

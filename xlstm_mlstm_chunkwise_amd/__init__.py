@@ -1,5 +1,6 @@
 """MI355X (gfx950) chunkwise mLSTM: Python binding of libmlstm_tfla.so (forward
-pass, backward pass and recurrent decode step).
+pass, backward pass and recurrent decode step; the same of the gated delta
+rule; the head norm behind either).
 
 The binding only marshals arguments: it allocates outputs and workspace with
 PyTorch (device memory), passes raw device pointers and the current HIP
@@ -54,6 +55,24 @@ class FwDesc(ctypes.Structure):
     ]
 
 
+class DeltaDesc(ctypes.Structure):
+    """Mirror of mlstm_delta_desc_t."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("NH", ctypes.c_int32), ("S", ctypes.c_int32),
+        ("DHQK", ctypes.c_int32), ("DHV", ctypes.c_int32), ("qkv_dtype", ctypes.c_int32),
+        ("h_dtype", ctypes.c_int32), ("qk_scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 4),
+    ]
+
+
+class HeadNormDesc(ctypes.Structure):
+    """Mirror of mlstm_head_norm_desc_t."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("NH", ctypes.c_int32), ("S", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32 * 3),
+    ]
+
+
 _lib = None
 _SYMBOLS = {
     "mlstm_abi_version": (ctypes.c_int, []),
@@ -86,6 +105,19 @@ _SYMBOLS = {
                            + [ctypes.c_size_t, ctypes.c_void_p]),
     "mlstm_bw_grads": (ctypes.c_int, [ctypes.POINTER(FwDesc)] + [ctypes.c_void_p] * 17
                        + [ctypes.c_size_t, ctypes.c_void_p]),
+    "mlstm_delta_validate": (ctypes.c_int, [ctypes.POINTER(DeltaDesc)]),
+    "mlstm_delta_fw_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(DeltaDesc)]),
+    "mlstm_delta_bw_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(DeltaDesc)]),
+    "mlstm_delta_fw": (ctypes.c_int, [ctypes.POINTER(DeltaDesc)] + [ctypes.c_void_p] * 9
+                       + [ctypes.c_size_t, ctypes.c_void_p]),
+    "mlstm_delta_bw": (ctypes.c_int, [ctypes.POINTER(DeltaDesc)] + [ctypes.c_void_p] * 15
+                       + [ctypes.c_size_t, ctypes.c_void_p]),
+    "mlstm_delta_step": (ctypes.c_int, [ctypes.POINTER(DeltaDesc)] + [ctypes.c_void_p] * 9),
+    "mlstm_head_norm_validate": (ctypes.c_int, [ctypes.POINTER(HeadNormDesc)]),
+    "mlstm_head_norm_bw_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(HeadNormDesc)]),
+    "mlstm_head_norm_fw": (ctypes.c_int, [ctypes.POINTER(HeadNormDesc)] + [ctypes.c_void_p] * 5),
+    "mlstm_head_norm_bw": (ctypes.c_int, [ctypes.POINTER(HeadNormDesc)] + [ctypes.c_void_p] * 7
+                           + [ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 
@@ -629,14 +661,16 @@ def mlstm_recurrent_step_q8(q, k, v, i_pre, f_pre, Cq=None, Cs=None, n=None, m=N
 
 def mlstm_chunkwise(q, k, v, i_pre, f_pre, C0=None, n0=None, m0=None, *, chunk_size: int, gate: str = "exp",
                     precision: str = "split", qk_scale: Optional[float] = None, eps: float = 0.0,
-                    tile_lq: int = 0, tile_lkv: int = 0, schedule: str = "auto"):
+                    tile_lq: int = 0, tile_lkv: int = 0, schedule: str = "auto", norm_weight=None, norm_bias=None,
+                    norm_eps: float = 1e-6):
     """H of the forward pass as a torch autograd function: the forward runs
     mlstm_chunkwise_fw, the backward mlstm_chunkwise_bw (gradients for q, k,
     v, i_pre, f_pre and, when given, C0, n0, m0).  H is float32.  The final
     state is not returned here: no gradient enters through it.  With the exp
     gate the forward also keeps the per-row m and normaliser, and the
     backward takes them with H instead of recomputing the intra-chunk pass
-    (mlstm_chunkwise_bw_saved)."""
+    (mlstm_chunkwise_bw_saved).  norm_weight (NH, DHV), with norm_bias or
+    without: return head_norm(H) instead, (B, S, NH, DHV) in q's dtype."""
     torch = _torch()
     kw = dict(chunk_size=chunk_size, gate=gate, precision=precision, qk_scale=qk_scale, eps=eps,
               tile_lq=tile_lq, tile_lkv=tile_lkv)
@@ -667,4 +701,314 @@ def mlstm_chunkwise(q, k, v, i_pre, f_pre, C0=None, n0=None, m0=None, *, chunk_s
                     g.get("dC0") if C0_ is not None else None, g.get("dn0") if n0_ is not None else None,
                     g.get("dm0") if m0_ is not None else None)
 
-    return _Fn.apply(q, k, v, i_pre, f_pre, C0, n0, m0)
+    H = _Fn.apply(q, k, v, i_pre, f_pre, C0, n0, m0)
+    return _normed(H, q, norm_weight, norm_bias, norm_eps)
+
+
+# ---------------------------------------------------------------------------
+# gated delta rule
+
+def make_delta_desc(B, NH, S, DHQK, DHV, *, qkv_dtype=MLSTM_BF16, h_dtype=MLSTM_F32, qk_scale=0.0) -> DeltaDesc:
+    d = DeltaDesc()
+    d.B, d.NH, d.S, d.DHQK, d.DHV = B, NH, S, DHQK, DHV
+    d.qkv_dtype, d.h_dtype, d.qk_scale = qkv_dtype, h_dtype, qk_scale
+    return d
+
+
+def delta_validate(desc: DeltaDesc) -> int:
+    return lib().mlstm_delta_validate(ctypes.byref(desc))
+
+
+def delta_fw_workspace_bytes(desc: DeltaDesc) -> int:
+    return lib().mlstm_delta_fw_workspace_bytes(ctypes.byref(desc))
+
+
+def delta_bw_workspace_bytes(desc: DeltaDesc) -> int:
+    return lib().mlstm_delta_bw_workspace_bytes(ctypes.byref(desc))
+
+
+def _out_code(dtype, name) -> int:
+    torch = _torch()
+    if dtype == torch.bfloat16:
+        return MLSTM_BF16
+    if dtype == torch.float32:
+        return MLSTM_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+
+
+def _check_same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _call(where, dev, *args):
+    """Run a C entry point on dev's current stream (appended as the last
+    argument); raises MlstmError for a non-zero status."""
+    torch = _torch()
+    fn = getattr(lib(), where)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+    if st:
+        raise MlstmError(st, where)
+
+
+def _bytes_of(need, workspace, dev):
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    size = workspace.numel() * workspace.element_size()
+    if size < need:
+        raise ValueError(f"workspace holds {size} bytes, need {need}")
+    return workspace, size
+
+
+def _delta_desc(where, q, v, lead, S, h_dtype, qk_scale):
+    desc = make_delta_desc(*lead, S, q.shape[-1], v.shape[-1], qkv_dtype=_dtype_code(q),
+                           h_dtype=_out_code(h_dtype, "h_dtype"), qk_scale=0.0 if qk_scale is None else float(qk_scale))
+    st = delta_validate(desc)
+    if st:
+        raise MlstmError(st, where)
+    return desc
+
+
+def mlstm_delta_fw(q, k, v, i_pre, f_pre, C0=None, *, h_dtype=None, qk_scale: Optional[float] = None,
+                   workspace=None, return_final_state: bool = True, out=None):
+    """Forward pass of the gated delta rule on the GPU (mlstm_delta_fw).
+
+    q, k: (B, NH, S, DHQK); v: (B, NH, S, DHV), bfloat16 or float32, DHQK 64,
+    128 or 256, DHV a multiple of 64 up to 512; i_pre, f_pre: (B, NH, S)
+    float32; C0 (B, NH, DHQK, DHV) float32 or None (zero state).  Returns
+    (H, C); C is None when return_final_state is False.  H is float32 unless
+    h_dtype or out says otherwise.  Keys are taken as they are: with
+    sigmoid(i_pre) |k|^2 < 2 the state stays bounded.
+    """
+    torch = _torch()
+    B, NH, S, DK, DV = _check_inputs(q, k, v, i_pre, f_pre)
+    h_dtype = h_dtype or (torch.float32 if out is None else out.dtype)
+    _check(C0, "C0", (B, NH, DK, DV), torch.float32)
+    _check(out, "H", (B, NH, S, DV), h_dtype)
+    dev = q.device
+    _check_same_device(dev, K=k, V=v, i_pre=i_pre, f_pre=f_pre, C0=C0, H=out, workspace=workspace)
+    desc = _delta_desc("mlstm_delta_fw", q, v, (B, NH), S, h_dtype, qk_scale)
+    workspace, ws_bytes = _bytes_of(delta_fw_workspace_bytes(desc), workspace, dev)
+    H = torch.empty((B, NH, S, DV), dtype=h_dtype, device=dev) if out is None else out
+    C = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev) if return_final_state else None
+    _call("mlstm_delta_fw", dev, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C0),
+          _ptr(H), _ptr(C), _ptr(workspace), ws_bytes)
+    return H, C
+
+
+def mlstm_delta_bw(q, k, v, i_pre, f_pre, dH, C0=None, dC=None, *, qk_scale: Optional[float] = None,
+                   state_grads: bool = False, workspace=None):
+    """Backward pass of the gated delta rule on the GPU (mlstm_delta_bw): the
+    gradients of sum(dH * H) + sum(dC * C) for mlstm_delta_fw(q, k, v, i_pre,
+    f_pre, C0).  dH has H's shape, bfloat16 or float32; dC (B, NH, DHQK, DHV)
+    float32 or None (no gradient enters through the final state).  Returns a
+    dict with dQ, dK, dV (q's dtype), d_i, d_f (float32) and, with
+    state_grads, dC0 (float32)."""
+    torch = _torch()
+    B, NH, S, DK, DV = _check_inputs(q, k, v, i_pre, f_pre)
+    _check(dH, "dH", (B, NH, S, DV))
+    _check(C0, "C0", (B, NH, DK, DV), torch.float32)
+    _check(dC, "dC", (B, NH, DK, DV), torch.float32)
+    dev = q.device
+    _check_same_device(dev, K=k, V=v, i_pre=i_pre, f_pre=f_pre, dH=dH, C0=C0, dC=dC, workspace=workspace)
+    desc = _delta_desc("mlstm_delta_bw", q, v, (B, NH), S, dH.dtype, qk_scale)
+    workspace, ws_bytes = _bytes_of(delta_bw_workspace_bytes(desc), workspace, dev)
+    g = dict(dQ=torch.empty_like(q), dK=torch.empty_like(k), dV=torch.empty_like(v), d_i=torch.empty_like(i_pre),
+             d_f=torch.empty_like(f_pre))
+    if state_grads:
+        g["dC0"] = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev)
+    _call("mlstm_delta_bw", dev, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C0),
+          _ptr(dH), _ptr(dC), _ptr(g["dQ"]), _ptr(g["dK"]), _ptr(g["dV"]), _ptr(g["d_i"]), _ptr(g["d_f"]),
+          _ptr(g.get("dC0")), _ptr(workspace), ws_bytes)
+    return g
+
+
+def mlstm_delta_step(q, k, v, i_pre, f_pre, C=None, *, h_dtype=None, qk_scale: Optional[float] = None, C_out=None):
+    """One time step of the gated delta rule for every head (decode) on the
+    GPU (mlstm_delta_step).  q, k: (B, NH, DHQK); v: (B, NH, DHV), bfloat16 or
+    float32; i_pre, f_pre: (B, NH) float32; C (B, NH, DHQK, DHV) float32 or
+    None (zero state), as mlstm_delta_fw returns it.  Returns (h, C'); C_out
+    may be C itself (updated in place)."""
+    torch = _torch()
+    if q.dim() != 3:
+        raise ValueError("q must be (B, NH, DHQK)")
+    B, NH, DK = q.shape
+    DV = v.shape[-1]
+    _check(q, "q", (B, NH, DK))
+    _check(k, "k", (B, NH, DK), q.dtype)
+    _check(v, "v", (B, NH, DV), q.dtype)
+    _check(i_pre, "i_pre", (B, NH), torch.float32)
+    _check(f_pre, "f_pre", (B, NH), torch.float32)
+    _check(C, "C", (B, NH, DK, DV), torch.float32)
+    _check(C_out, "C_out", (B, NH, DK, DV), torch.float32)
+    dev = q.device
+    _check_same_device(dev, k=k, v=v, i_pre=i_pre, f_pre=f_pre, C=C, C_out=C_out)
+    h_dtype = h_dtype or torch.float32
+    desc = _delta_desc("mlstm_delta_step", q, v, (B, NH), 1, h_dtype, qk_scale)
+    h = torch.empty((B, NH, DV), dtype=h_dtype, device=dev)
+    if C_out is None:
+        C_out = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev)
+    _call("mlstm_delta_step", dev, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C),
+          _ptr(h), _ptr(C_out))
+    return h, C_out
+
+
+_functions = {}
+
+
+def _delta_function():
+    """The autograd function of mlstm_delta (torch is imported on first use)."""
+    torch = _torch()
+    if "delta" not in _functions:
+        class MlstmDelta(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, v, i_pre, f_pre, C0, h_dtype, qk_scale, final_state):
+                H, C = mlstm_delta_fw(q, k, v, i_pre, f_pre, C0, h_dtype=h_dtype, qk_scale=qk_scale,
+                                      return_final_state=final_state)
+                ctx.save_for_backward(q, k, v, i_pre, f_pre, C0)
+                ctx.set_materialize_grads(False)
+                ctx.h_like, ctx.qk_scale = (H.shape, H.dtype), qk_scale
+                return (H, C) if final_state else H
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dH, dC=None):
+                q, k, v, i_pre, f_pre, C0 = ctx.saved_tensors
+                if dH is None and dC is None:
+                    return (None,) * 9
+                if dH is None:
+                    dH = torch.zeros(ctx.h_like[0], dtype=ctx.h_like[1], device=q.device)
+                g = mlstm_delta_bw(q, k, v, i_pre, f_pre, dH.contiguous(), C0, None if dC is None else dC.contiguous(),
+                                   qk_scale=ctx.qk_scale, state_grads=ctx.needs_input_grad[5])
+                return g["dQ"], g["dK"], g["dV"], g["d_i"], g["d_f"], g.get("dC0"), None, None, None
+
+        _functions["delta"] = MlstmDelta
+    return _functions["delta"]
+
+
+def mlstm_delta(q, k, v, i_pre, f_pre, C0=None, *, h_dtype=None, qk_scale: Optional[float] = None,
+                return_final_state: bool = False, norm_weight=None, norm_bias=None, norm_eps: float = 1e-6):
+    """The gated delta rule as a torch autograd function: the forward runs
+    mlstm_delta_fw, the backward mlstm_delta_bw (gradients for q, k, v, i_pre,
+    f_pre and C0).  Returns H, or (H, C) with return_final_state; gradients
+    flow in through both.  norm_weight (NH, DHV), with norm_bias or without:
+    head_norm(H) takes H's place, (B, S, NH, DHV) in q's dtype."""
+    out = _delta_function().apply(q, k, v, i_pre, f_pre, C0, h_dtype, qk_scale, return_final_state)
+    H, C = out if return_final_state else (out, None)
+    H = _normed(H, q, norm_weight, norm_bias, norm_eps)
+    return (H, C) if return_final_state else H
+
+
+# ---------------------------------------------------------------------------
+# head norm
+
+def make_head_norm_desc(B, NH, S, D, *, x_dtype=MLSTM_F32, y_dtype=MLSTM_F32, eps=1e-6) -> HeadNormDesc:
+    d = HeadNormDesc()
+    d.B, d.NH, d.S, d.D, d.x_dtype, d.y_dtype, d.eps = B, NH, S, D, x_dtype, y_dtype, eps
+    return d
+
+
+def head_norm_validate(desc: HeadNormDesc) -> int:
+    return lib().mlstm_head_norm_validate(ctypes.byref(desc))
+
+
+def head_norm_bw_workspace_bytes(desc: HeadNormDesc) -> int:
+    return lib().mlstm_head_norm_bw_workspace_bytes(ctypes.byref(desc))
+
+
+def _norm_desc(where, x, y_dtype, eps):
+    if x.dim() != 4:
+        raise ValueError("x must be (B, NH, S, D)")
+    desc = make_head_norm_desc(*x.shape, x_dtype=_out_code(x.dtype, "x"), y_dtype=_out_code(y_dtype, "y_dtype"),
+                               eps=float(eps))
+    st = head_norm_validate(desc)
+    if st:
+        raise MlstmError(st, where)
+    return desc
+
+
+def head_norm_fw(x, weight=None, bias=None, *, eps: float = 1e-6, y_dtype=None, out=None):
+    """Layer norm of every row of x (B, NH, S, D), the cell's output H, over
+    its D values on the GPU (mlstm_head_norm_fw), with weight and bias (NH, D)
+    float32 or None.  Returns y (B, S, NH, D), the layout of the output
+    projection, in y_dtype (x's dtype unless given); D is a multiple of 64 up
+    to 512, x and y bfloat16 or float32."""
+    torch = _torch()
+    y_dtype = y_dtype or (x.dtype if out is None else out.dtype)
+    desc = _norm_desc("mlstm_head_norm_fw", x, y_dtype, eps)
+    B, NH, S, D = x.shape
+    _check(x, "x", (B, NH, S, D))
+    _check(weight, "weight", (NH, D), torch.float32)
+    _check(bias, "bias", (NH, D), torch.float32)
+    _check(out, "y", (B, S, NH, D), y_dtype)
+    dev = x.device
+    _check_same_device(dev, weight=weight, bias=bias, y=out)
+    y = torch.empty((B, S, NH, D), dtype=y_dtype, device=dev) if out is None else out
+    _call("mlstm_head_norm_fw", dev, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y))
+    return y
+
+
+def head_norm_bw(x, dy, weight=None, *, eps: float = 1e-6, weight_grads: bool = True, workspace=None):
+    """Backward pass of head_norm_fw on the GPU (mlstm_head_norm_bw): (dx,
+    dweight, dbias) from x, dy (B, S, NH, D) and the weight; dx in x's dtype,
+    dweight and dbias (NH, D) float32, None without weight_grads."""
+    torch = _torch()
+    desc = _norm_desc("mlstm_head_norm_bw", x, dy.dtype, eps)
+    B, NH, S, D = x.shape
+    _check(x, "x", (B, NH, S, D))
+    _check(dy, "dy", (B, S, NH, D))
+    _check(weight, "weight", (NH, D), torch.float32)
+    dev = x.device
+    _check_same_device(dev, dy=dy, weight=weight, workspace=workspace)
+    dx, dw, db, ws_bytes = torch.empty_like(x), None, None, 0
+    if weight_grads:
+        workspace, ws_bytes = _bytes_of(head_norm_bw_workspace_bytes(desc), workspace, dev)
+        dw, db = (torch.empty((NH, D), dtype=torch.float32, device=dev) for _ in range(2))
+    _call("mlstm_head_norm_bw", dev, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
+          _ptr(workspace), ws_bytes)
+    return dx, dw, db
+
+
+def _head_norm_function():
+    """The autograd function of head_norm."""
+    torch = _torch()
+    if "norm" not in _functions:
+        class HeadNorm(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, weight, bias, eps, y_dtype):
+                ctx.save_for_backward(x, weight)
+                ctx.eps = eps
+                return head_norm_fw(x, weight, bias, eps=eps, y_dtype=y_dtype)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy):
+                x, weight = ctx.saved_tensors
+                need = ctx.needs_input_grad
+                dx, dw, db = head_norm_bw(x, dy.contiguous(), weight, eps=ctx.eps, weight_grads=need[1] or need[2])
+                return dx, dw if need[1] else None, db if need[2] else None, None, None
+
+        _functions["norm"] = HeadNorm
+    return _functions["norm"]
+
+
+def head_norm(x, weight=None, bias=None, *, eps: float = 1e-6, y_dtype=None):
+    """head_norm_fw as a torch autograd function (gradients for x, weight and
+    bias by mlstm_head_norm_bw)."""
+    return _head_norm_function().apply(x, weight, bias, eps, y_dtype)
+
+
+def _normed(H, q, weight, bias, eps):
+    if weight is None:
+        if bias is not None:
+            raise ValueError("norm_bias needs norm_weight")
+        return H
+    return head_norm(H, weight, bias, eps=eps, y_dtype=q.dtype)

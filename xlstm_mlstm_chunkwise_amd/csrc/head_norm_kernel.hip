@@ -1,0 +1,233 @@
+// Head norm: the layer norm of every row of H over its D values, with a
+// weight and a bias per head and channel, gfx950.
+//   n = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),  y = w n + c
+//   g = w dy,  dx = rstd (g - mean(g) - n mean(g n))
+//   dw = sum over the head's rows of dy n,  dc = the same sum of dy
+// x and dx are (B, NH, S, D), y and dy (B, S, NH, D): the norm also turns the
+// cell's layout into the one of the projection behind it, so no transposed
+// copy is made.
+//
+// Both passes are bound by memory.  A row is held in registers by 8, 16, 32
+// or 64 lanes, eight values each, and read once; mean and variance take two
+// passes over the registers.  The backward pass forms them again from x,
+// which it reads anyhow, instead of reading saved ones.  Its workgroups take
+// the rows of one head, keep their sums of dy n and dy in registers, and
+// leave one partial sum each; a second kernel adds the partial sums in a
+// fixed order, so that equal inputs give equal bits.
+#include "delta_common.h"
+#include "kernels.h"
+
+namespace mlstm {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void load8f(const void* p, size_t i, bool bf16, float (&x)[8]) {
+  if (bf16) Ops<bf16_t>::load8(static_cast<const bf16_t*>(p) + i, x);
+  else Ops<float>::load8(static_cast<const float*>(p) + i, x);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8f(T* p, const float (&x)[8]) {
+  store4(p, x[0], x[1], x[2], x[3]);
+  store4(p + 4, x[4], x[5], x[6], x[7]);
+}
+template <>
+__device__ __forceinline__ void store8f<bf16_t>(bf16_t* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(round_bf16x2(x[0], x[1]), round_bf16x2(x[2], x[3]),
+                                            round_bf16x2(x[4], x[5]), round_bf16x2(x[6], x[7]));
+}
+
+// Sum over the LPR lanes of a row.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+  return x;
+}
+
+// n and rstd of a row held eight values a lane; `in`: the lane has values.
+template <int LPR>
+__device__ __forceinline__ float normalise(float (&x)[8], bool in, float inv_d, float eps) {
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s += x[e];
+  const float mean = row_sum<LPR>(in ? s : 0.0f) * inv_d;
+  float q = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] -= mean;
+    q += x[e] * x[e];
+  }
+  const float rstd = 1.0f / sqrtf(row_sum<LPR>(in ? q : 0.0f) * inv_d + eps);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= rstd;
+  return rstd;
+}
+
+template <typename TX, typename TY, int LPR>
+__global__ __launch_bounds__(kThreads) void head_norm_kernel(const HeadNormParams p) {
+  constexpr int RPB = kThreads / LPR;  // rows a workgroup
+  const long long r = (long long)blockIdx.x * RPB + threadIdx.x / LPR;
+  const int d = 8 * (threadIdx.x % LPR);
+  const bool in = d < p.D;
+  const bool row_in = r < (long long)p.B * p.NH * p.S;
+  float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (in && row_in) Ops<TX>::load8(static_cast<const TX*>(p.x) + (size_t)r * p.D + d, x);
+  normalise<LPR>(x, in, 1.0f / (float)p.D, p.eps);
+  if (!in || !row_in) return;
+  const int h = (int)((r / p.S) % p.NH);
+  const long long b = r / p.S / p.NH, t = r % p.S;
+  if (p.weight) {
+    float w[8];
+    Ops<float>::load8(p.weight + (size_t)h * p.D + d, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= w[e];
+  }
+  if (p.bias) {
+    float c[8];
+    Ops<float>::load8(p.bias + (size_t)h * p.D + d, c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += c[e];
+  }
+  store8f(static_cast<TY*>(p.y) + (size_t)((b * p.S + t) * p.NH + h) * p.D + d, x);
+}
+
+template <typename TX, typename TY, int LPR>
+__global__ __launch_bounds__(kThreads) void head_norm_back_kernel(const HeadNormParams p) {
+  constexpr int RPB = kThreads / LPR;
+  __shared__ float s_sum[2][RPB][8 * LPR];
+  const int h = blockIdx.x % p.NH, blk = blockIdx.x / p.NH;
+  const int g = threadIdx.x / LPR, d = 8 * (threadIdx.x % LPR);
+  const bool in = d < p.D;
+  const float inv_d = 1.0f / (float)p.D;
+  float w[8], dw[8], dc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    w[e] = 1.0f;
+    dw[e] = dc[e] = 0.0f;
+  }
+  if (in && p.weight) Ops<float>::load8(p.weight + (size_t)h * p.D + d, w);
+  const long long rows = (long long)p.B * p.S;
+  // the same trip count for every lane: the sums of a row run over lanes
+  for (long long i0 = (long long)blk * RPB; i0 < rows; i0 += (long long)p.blocks * RPB) {
+    const long long i = i0 + g;
+    const bool ok = in && i < rows;
+    const long long b = i / p.S, t = i % p.S;
+    float n[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, dy[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    const size_t ox = (size_t)((b * p.NH + h) * p.S + t) * p.D + d;
+    if (ok) {
+      Ops<TX>::load8(static_cast<const TX*>(p.x) + ox, n);
+      Ops<TY>::load8(static_cast<const TY*>(p.dy) + (size_t)(i * p.NH + h) * p.D + d, dy);
+    }
+    const float rstd = normalise<LPR>(n, in, inv_d, p.eps);
+    float sg = 0.0f, sgn = 0.0f, gw[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      gw[e] = w[e] * dy[e];
+      sg += gw[e];
+      sgn += gw[e] * n[e];
+    }
+    sg = row_sum<LPR>(ok ? sg : 0.0f) * inv_d;
+    sgn = row_sum<LPR>(ok ? sgn : 0.0f) * inv_d;
+    if (ok) {
+      float dx[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dx[e] = rstd * (gw[e] - sg - n[e] * sgn);
+        dw[e] += dy[e] * n[e];
+        dc[e] += dy[e];
+      }
+      store8f(static_cast<TX*>(p.dx) + ox, dx);
+    }
+  }
+  if (!p.partial) return;
+  Ops<float>::store8(&s_sum[0][g][d], dw);
+  Ops<float>::store8(&s_sum[1][g][d], dc);
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * p.D; i += kThreads) {
+    const int which = i / p.D, dd = i % p.D;
+    float s = 0.0f;
+    for (int k = 0; k < RPB; ++k) s += s_sum[which][k][dd];
+    p.partial[(((size_t)blk * p.NH + h) * 2 + which) * p.D + dd] = s;
+  }
+}
+
+// The partial sums of one (head, which, channel), added in the order of their
+// workgroups: four runs, one a wave, then the runs.
+__global__ __launch_bounds__(kThreads) void head_norm_sum_kernel(const HeadNormParams p) {
+  __shared__ float s_run[4][64];
+  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
+  const size_t n = (size_t)p.NH * 2 * p.D, i = (size_t)blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (i < n)
+    for (int k = run; k < p.blocks; k += 4) s += p.partial[(size_t)k * n + i];
+  s_run[run][lane] = s;
+  __syncthreads();
+  if (run || i >= n) return;
+  s = (s_run[0][lane] + s_run[1][lane]) + (s_run[2][lane] + s_run[3][lane]);
+  const size_t h = i / (2 * p.D), which = i / p.D % 2, d = i % p.D;
+  float* out = which ? p.dbias : p.dweight;
+  if (out) out[h * p.D + d] = s;
+}
+
+template <typename TX, typename TY, int LPR>
+hipError_t launch_rows(const HeadNormParams& p, bool back, hipStream_t stream) {
+  const long long rpb = kThreads / LPR;
+  if (back) {
+    hipLaunchKernelGGL((head_norm_back_kernel<TX, TY, LPR>), dim3((unsigned)((long long)p.blocks * p.NH)), dim3(kThreads),
+                       0, stream, p);
+  } else {
+    const long long rows = (long long)p.B * p.NH * p.S;
+    hipLaunchKernelGGL((head_norm_kernel<TX, TY, LPR>), dim3((unsigned)((rows + rpb - 1) / rpb)), dim3(kThreads), 0,
+                       stream, p);
+  }
+  return hipGetLastError();
+}
+
+template <typename TX, typename TY>
+hipError_t launch_types(const HeadNormParams& p, bool back, hipStream_t stream) {
+  switch (head_norm_lanes(p.D)) {
+    case 8: return launch_rows<TX, TY, 8>(p, back, stream);
+    case 16: return launch_rows<TX, TY, 16>(p, back, stream);
+    case 32: return launch_rows<TX, TY, 32>(p, back, stream);
+    case 64: return launch_rows<TX, TY, 64>(p, back, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch(const HeadNormParams& p, bool back, hipStream_t stream) {
+  if (p.x_bf16)
+    return p.y_bf16 ? launch_types<bf16_t, bf16_t>(p, back, stream) : launch_types<bf16_t, float>(p, back, stream);
+  return p.y_bf16 ? launch_types<float, bf16_t>(p, back, stream) : launch_types<float, float>(p, back, stream);
+}
+
+}  // namespace
+
+int head_norm_lanes(int D) {
+  int n = 8;
+  while (n < D / 8) n *= 2;
+  return n;
+}
+
+// Enough workgroups to fill the chip eight times over, no more than there are
+// rows for, and few enough that the partial sums stay small next to the rows.
+int head_norm_blocks(int B, int NH, int S, int D) {
+  const long long rpb = kThreads / head_norm_lanes(D), rows = (long long)B * S;
+  long long n = (rows + 4 * rpb - 1) / (4 * rpb);
+  const long long most = NH < 2048 ? 2048 / NH : 1;
+  if (n > most) n = most;
+  return (int)(n < 1 ? 1 : n);
+}
+
+hipError_t launch_head_norm(const HeadNormParams& p, hipStream_t stream) { return launch(p, false, stream); }
+
+hipError_t launch_head_norm_back(const HeadNormParams& p, hipStream_t stream) {
+  hipError_t e = launch(p, true, stream);
+  if (e != hipSuccess || !p.partial) return e;
+  const size_t n = (size_t)p.NH * 2 * p.D;
+  hipLaunchKernelGGL(head_norm_sum_kernel, dim3((unsigned)((n + 63) / 64)), dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace mlstm

@@ -246,4 +246,84 @@ hipError_t launch_hintra_f64m(const HintraParams& p, bool bf16_inputs, bool sig,
 hipError_t launch_unpack_states(const void* packed, float* C, long long n_states, int DK, int DV,
                                 hipStream_t stream, const float* scales = nullptr);
 
+// Gated delta rule (delta_*_kernel.hip).  A chunk has 64 rows for bf16
+// inputs and 32 for float32 ones; at = bh * Nc + chunk below.
+constexpr int kDeltaChunkBf16 = 64, kDeltaChunkF32 = 32;
+// log a below this counts as this: e^ of it is zero in float32.
+constexpr float kMinLogDecay = -200.0f;
+
+struct DeltaParams {
+  const void* Q;  // (BH, S, DK), bf16 or float32
+  const void* K;
+  const void* V;  // (BH, S, DV)
+  const float* i_pre;  // (BH, S)
+  const float* f_pre;
+  const float* C0;  // (BH, DK, DV), may be null (zero state)
+  void* H;          // (BH, S, DV), bf16 or float32
+  float* C_out;     // may be null
+  const void* dH;   // (BH, S, DV), type of H
+  const float* dC_out;  // may be null (zero)
+  void* dQ;  // type of Q
+  void* dK;
+  void* dV;
+  float* d_i;
+  float* d_f;
+  float* dC0;  // may be null
+  // workspace
+  float* T;      // (at, L, L)
+  float* P;      // (at, L, L)
+  double* bsum;  // (at, L) sum of log a within the chunk
+  float* e;      // (at, L) e^bsum
+  float* w;      // (at, L) e^(bsum of the last row - bsum)
+  float* C_states;  // (at, DK, DV) state entering the chunk (backward)
+  float* G_states;  // (at, DK, DV) gradient of the state behind the chunk
+  float* U;         // (at, L, DV)
+  float* R;         // (at, L, DV) gradient of V in float32
+  float* anchor;    // (at, DV / 16) partial sums of w u . (K G)
+  float scale;
+  int BH, S, DK, DV, Nc;
+  int qkv_bf16, h_bf16;
+};
+
+enum class DeltaWalk { kForward, kStates, kBack };
+hipError_t launch_delta_prep(const DeltaParams& p, hipStream_t stream);
+hipError_t launch_delta_walk(const DeltaParams& p, DeltaWalk what, hipStream_t stream);
+hipError_t launch_delta_grads(const DeltaParams& p, hipStream_t stream);
+
+struct DeltaStepParams {
+  const void* q;  // (BH, DK), bf16 or float32
+  const void* k;
+  const void* v;  // (BH, DV)
+  const float* i_pre;  // (BH)
+  const float* f_pre;
+  const float* C_in;  // (BH, DK, DV), may be null (zero state); may equal C_out
+  void* h;            // (BH, DV), bf16 or float32
+  float* C_out;
+  float scale;
+  int BH, DK, DV;
+  int qkv_bf16, h_bf16;
+};
+hipError_t launch_delta_step(const DeltaStepParams& p, hipStream_t stream);
+
+// Head norm (head_norm_kernel.hip).
+struct HeadNormParams {
+  const void* x;        // (B, NH, S, D), bf16 or float32
+  const float* weight;  // (NH, D), may be null (ones)
+  const float* bias;    // (NH, D), may be null (zeros)
+  void* y;              // (B, S, NH, D), bf16 or float32
+  const void* dy;       // type of y
+  void* dx;             // type of x
+  float* dweight;       // (NH, D), may be null
+  float* dbias;         // (NH, D), may be null
+  float* partial;       // (blocks, NH, 2, D), null when neither sum is wanted
+  float eps;
+  int B, NH, S, D;
+  int blocks;  // workgroups a head of the backward pass
+  int x_bf16, y_bf16;
+};
+int head_norm_lanes(int D);
+int head_norm_blocks(int B, int NH, int S, int D);
+hipError_t launch_head_norm(const HeadNormParams& p, hipStream_t stream);
+hipError_t launch_head_norm_back(const HeadNormParams& p, hipStream_t stream);
+
 }  // namespace mlstm
