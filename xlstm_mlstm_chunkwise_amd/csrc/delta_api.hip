@@ -47,7 +47,7 @@ int validate(const mlstm_delta_desc_t* d) {
 }
 
 struct Layout {
-  size_t T, P, bsum, e, w, fw_total, C, G, U, R, anchor, bw_total;
+  size_t T, P, bsum, e, w, fw_total, Tt, C, G, U, R, anchor, bw_total;
 };
 
 Layout layout(const mlstm_delta_desc_t* d) {
@@ -60,12 +60,14 @@ Layout layout(const mlstm_delta_desc_t* d) {
     off += round_up(bytes);
     return at;
   };
-  l.T = take(n * L * L * sizeof(float));
-  l.P = take(n * L * L * sizeof(float));
+  const size_t square = mlstm::delta_square_bytes((int)L);
+  l.T = take(n * square);
+  l.P = take(n * square);
   l.bsum = take(n * L * sizeof(double));
   l.e = take(n * L * sizeof(float));
   l.w = take(n * L * sizeof(float));
   l.fw_total = off;
+  l.Tt = take(n * square);
   l.C = take(n * state * sizeof(float));
   l.G = take(n * state * sizeof(float));
   l.U = take(n * L * d->DHV * sizeof(float));
@@ -87,8 +89,8 @@ mlstm::DeltaParams params(const mlstm_delta_desc_t* d, const Layout& l, const vo
   p.f_pre = f_pre;
   p.C0 = C0;
   if (ws) {
-    p.T = at(l.T);
-    p.P = at(l.P);
+    p.T = reinterpret_cast<uint16_t*>(ws + l.T);
+    p.P = reinterpret_cast<uint16_t*>(ws + l.P);
     p.bsum = reinterpret_cast<double*>(ws + l.bsum);
     p.e = at(l.e);
     p.w = at(l.w);
@@ -168,7 +170,7 @@ int mlstm_delta_fw(const mlstm_delta_desc_t* desc, const void* Q, const void* K,
   p.H = H;
   p.C_out = C_out;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = p.Nc ? mlstm::launch_delta_prep(p, s) : hipSuccess;
+  hipError_t e = p.Nc ? mlstm::launch_delta_prep(p, false, s) : hipSuccess;
   if (e == hipSuccess && (p.Nc || C_out)) e = mlstm::launch_delta_walk(p, mlstm::DeltaWalk::kForward, s);
   return status(e);
 }
@@ -188,6 +190,7 @@ int mlstm_delta_bw(const mlstm_delta_desc_t* desc, const void* Q, const void* K,
   mlstm::DeltaParams p = params(desc, l, Q, K, V, i_pre, f_pre, C0, workspace);
   char* ws = static_cast<char*>(workspace);
   if (ws) {
+    p.Tt = reinterpret_cast<uint16_t*>(ws + l.Tt);
     p.C_states = reinterpret_cast<float*>(ws + l.C);
     p.G_states = reinterpret_cast<float*>(ws + l.G);
     p.U = reinterpret_cast<float*>(ws + l.U);
@@ -205,7 +208,7 @@ int mlstm_delta_bw(const mlstm_delta_desc_t* desc, const void* Q, const void* K,
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = hipSuccess;
   if (p.Nc) {
-    e = mlstm::launch_delta_prep(p, s);
+    e = mlstm::launch_delta_prep(p, true, s);
     if (e == hipSuccess) e = mlstm::launch_delta_walk(p, mlstm::DeltaWalk::kStates, s);
   }
   if (e == hipSuccess && (p.Nc || dC0)) e = mlstm::launch_delta_walk(p, mlstm::DeltaWalk::kBack, s);

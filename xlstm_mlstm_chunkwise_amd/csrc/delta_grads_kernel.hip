@@ -15,7 +15,10 @@
 // One workgroup per chunk, DHQK / 32 waves: wave i owns rows 32 i .. 32 i + 31
 // of C and G, which it reads from memory straight into its operands, and
 // forms dQ^T and dK^T for them; the 64 x 64 products are spread over the
-// waves.  dH, U and dV go through LDS in steps of 32 value columns.
+// waves.  dH, U and dV go through LDS in steps of 32 value columns, two
+// buffers deep, with w U and -e dV cut into parts beside them, so that both
+// terms of dK add into one accumulator.  Every load is issued a step ahead:
+// without that the step took the latency of memory three times over.
 #include "delta_common.h"
 #include "kernels.h"
 
@@ -32,30 +35,81 @@ __device__ __forceinline__ void lower_tile(int i, int& rt, int& ct) {
 template <typename TIn, typename TH, int DK>
 struct GradLds {
   static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts, NH = DeltaIn<TH>::kParts;
-  static constexpr int kLdT = 40, kPlaneT = L * kLdT;   // 32 value columns of dH, U, dV
-  static constexpr int kLd = DK + 8, kPlane = L * kLd;  // K, Q (in the same space afterwards)
-  static constexpr int kLdS = L + 8, kPlaneS = L * kLdS;  // dP and dA + dA^T
-  static constexpr int kStage = (NH + 6) * kPlaneT > 2 * NP * kPlane ? (NH + 6) * kPlaneT : 2 * NP * kPlane;
-  static constexpr int kBytes = 2 * (kStage + 2 * 3 * kPlaneS);
+  static constexpr int NB = NP == 1 ? 2 : 3;  // parts of the terms of dK alone, which is stored as TIn
+  static constexpr int kLdT = 40, kPlaneT = L * kLdT;  // 32 value columns
+  // planes of a step: dH, U, dV, w U, -e dV
+  static constexpr int kU = NH * kPlaneT, kR = kU + 3 * kPlaneT, kUw = kR + NB * kPlaneT, kRe = kUw + NB * kPlaneT;
+  static constexpr int kStage = kRe + NB * kPlaneT;
+  // behind the last step, in the same space: K, Q, dP and dA + dA^T
+  static constexpr int kLd = DK + 8, kPlane = L * kLd, kLdS = L + 8, kPlaneS = L * kLdS;
+  static constexpr int kAfter = 2 * NP * kPlane + 2 * 3 * kPlaneS;
+  static constexpr int kBytes = 2 * (2 * kStage > kAfter ? 2 * kStage : kAfter);
 };
 
+// This lane's part of 32 value columns of sixteen rows of C or G: eight
+// consecutive values.
+struct StateRows {
+  words4_t x[2][2];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int lane_off, int row16, int v0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        x[i][h] = __builtin_bit_cast(
+            words4_t, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off + 16 * h, i * row16 + 4 * v0, 0));
+  }
+  __device__ __forceinline__ void values(int i, float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[i][e >> 2][e & 3]);
+  }
+};
+
+// Four values of a row in memory, zeros where `in` is false.
+template <typename T>
+struct Quad {
+  words4_t x;
+  __device__ __forceinline__ void load(const T* p, bool in) {
+    x = (words4_t){0u, 0u, 0u, 0u};
+    if (!in) return;
+    if constexpr (sizeof(T) == 2) {
+      const words2_t w = *reinterpret_cast<const words2_t*>(p);
+      x[0] = w[0];
+      x[1] = w[1];
+    } else {
+      x = *reinterpret_cast<const words4_t*>(p);
+    }
+  }
+  __device__ __forceinline__ float4_t values() const {
+    if constexpr (sizeof(T) == 2)
+      return (float4_t){__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
+                        __uint_as_float(x[1] & 0xffff0000u)};
+    else
+      return __builtin_bit_cast(float4_t, x);
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void store_quads(uint16_t* p, int plane, const float4_t& x) {
+  uint2 w[N];
+  split4<N>(x, w);
+#pragma unroll
+  for (int n = 0; n < N; ++n) *reinterpret_cast<uint2*>(p + n * plane) = w[n];
+}
+
 template <typename TIn, typename TH, int DK>
-__global__ __launch_bounds__(2 * DK) void delta_grads_kernel(const DeltaParams p) {
+__global__ __launch_bounds__(2 * DK) __attribute__((amdgpu_waves_per_eu(DK == 256 ? 2 : 1, DK == 256 ? 2 : 4))) void
+delta_grads_kernel(const DeltaParams p) {
   typedef GradLds<TIn, TH, DK> W;
-  constexpr int L = W::L, NP = W::NP, NH = W::NH, NW = DK / 32, THREADS = 64 * NW;
+  constexpr int L = W::L, NP = W::NP, NH = W::NH, NB = W::NB, NW = DK / 32, THREADS = 64 * NW;
   constexpr int RT = L / 16, NT = RT * (RT + 1) / 2, TPW = (NT + NW - 1) / NW;
-  constexpr int NB = NP == 1 ? 2 : 3;  // parts of the terms of dK alone, which is stored as TIn
-  constexpr int ROWS = (4 * L + THREADS - 1) / THREADS;
+  constexpr int QUADS = 8 * L, ROWS = (QUADS + THREADS - 1) / THREADS;
   __shared__ uint4 smem[W::kBytes / 16];
   __shared__ float s_red[NW][L];
   __shared__ float s_dvu[L], s_vdv[L], s_cg[NW];
   __shared__ double s_b[L];
-  uint16_t* s_H = reinterpret_cast<uint16_t*>(smem);
-  uint16_t* s_U = s_H + NH * W::kPlaneT;
-  uint16_t* s_R = s_U + 3 * W::kPlaneT;
   uint16_t* s_K = reinterpret_cast<uint16_t*>(smem);
   uint16_t* s_Q = s_K + NP * W::kPlane;
-  uint16_t* s_dP = reinterpret_cast<uint16_t*>(smem) + W::kStage;
+  uint16_t* s_dP = s_Q + NP * W::kPlane;
   uint16_t* s_dA = s_dP + 3 * W::kPlaneS;
 
   const int bh = blockIdx.x / p.Nc, c = blockIdx.x % p.Nc, t0 = c * L;
@@ -65,66 +119,102 @@ __global__ __launch_bounds__(2 * DK) void delta_grads_kernel(const DeltaParams p
   const int DV = p.DV;
   if (tid < L) s_b[tid] = p.bsum[at * L + tid];
 
-  float4_t dq[2][RT], dkc[2][RT], dkg[2][RT], hu[TPW], ru[TPW];
+  float4_t dq[2][RT], dk[2][RT], hu[TPW], ru[TPW];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < RT; ++j) dq[i][j] = dkc[i][j] = dkg[i][j] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < RT; ++j) dq[i][j] = dk[i][j] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < TPW; ++i) hu[i] = ru[i] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-  float cg = 0.0f, dvu[ROWS], vdv[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) dvu[i] = vdv[i] = 0.0f;
+  float cg = 0.0f, dvu[ROWS], vdv[ROWS], qe[ROWS], qw[ROWS];
 
-  const float* Cs = p.C_states + (at * DK + 32 * wave + row) * DV + 8 * grp;
-  const float* Gs = p.G_states + (at * DK + 32 * wave + row) * DV + 8 * grp;
-  for (int v0 = 0; v0 < DV; v0 += 32) {
-    float xc[2][8], xg[2][8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      Ops<float>::load8(Cs + (size_t)16 * i * DV + v0, xc[i]);
-      Ops<float>::load8(Gs + (size_t)16 * i * DV + v0, xg[i]);
-    }
-    __syncthreads();
+  // this wave's 32 rows of the states, this thread's quads of the rest
+  const uint32_t rows_bytes = 32u * (uint32_t)DV * 4u;
+  const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.C_states + (at * DK + 32 * __builtin_amdgcn_readfirstlane(wave)) * DV, rows_bytes);
+  const __amdgpu_buffer_rsrc_t rg = make_rsrc(p.G_states + (at * DK + 32 * __builtin_amdgcn_readfirstlane(wave)) * DV, rows_bytes);
+  const int state_off = 4 * (row * DV + 8 * grp), row16 = 64 * DV;
+  StateRows xc, xg, nc, ng;
+  Quad<float> qu[ROWS], qr[ROWS];
+  Quad<TH> qh[ROWS];
+  Quad<TIn> qv[ROWS];
+  auto fetch = [&](int v0) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int piece = tid + i * THREADS;
-      if (piece >= 4 * L) break;
-      const int t = piece >> 2, cc = v0 + 8 * (piece & 3), o = t * W::kLdT + 8 * (piece & 3);
-      float xu[8], xr[8];
-      Ops<float>::load8(p.U + (at * L + t) * DV + cc, xu);
-      Ops<float>::load8(p.R + (at * L + t) * DV + cc, xr);
-      store_parts<3>(s_U + o, W::kPlaneT, split_parts<3>(xu));
-      store_parts<3>(s_R + o, W::kPlaneT, split_parts<3>(xr));
-      const size_t g = ((size_t)bh * p.S + t0 + t) * DV + cc;
-      const bool in = t0 + t < p.S;
-      store_parts<NH>(s_H + o, W::kPlaneT, in ? load_parts(static_cast<const TH*>(p.dH) + g) : zero_parts<NH>());
-      float xv[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      if (in) Ops<TIn>::load8(static_cast<const TIn*>(p.V) + g, xv);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dvu[i] += xr[e] * xu[e];
-        vdv[i] += xv[e] * xr[e];
-      }
+      const int quad = tid + i * THREADS, t = quad >> 3, cc = v0 + 4 * (quad & 7);
+      const bool in = quad < QUADS, in_seq = in && t0 + t < p.S;
+      const size_t o = (at * L + t) * DV + cc, g = ((size_t)bh * p.S + t0 + t) * DV + cc;
+      qu[i].load(p.U + o, in);
+      qr[i].load(p.R + o, in);
+      qh[i].load(static_cast<const TH*>(p.dH) + g, in_seq);
+      qv[i].load(static_cast<const TIn*>(p.V) + g, in_seq);
     }
-    __syncthreads();
+  };
+  auto stage = [&](uint16_t* s) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int quad = tid + i * THREADS, o = (quad >> 3) * W::kLdT + 4 * (quad & 7);
+      const float4_t u = qu[i].values(), r = qr[i].values(), v = qv[i].values();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        dvu[i] += r[e] * u[e];
+        vdv[i] += v[e] * r[e];
+      }
+      if (QUADS % THREADS != 0 && quad >= QUADS) continue;
+      if constexpr (NH == 1)
+        *reinterpret_cast<words2_t*>(s + o) = (words2_t){qh[i].x[0], qh[i].x[1]};
+      else
+        store_quads<3>(s + o, W::kPlaneT, qh[i].values());
+      store_quads<3>(s + W::kU + o, W::kPlaneT, u);
+      store_quads<NB>(s + W::kR + o, W::kPlaneT, r);
+      store_quads<NB>(s + W::kUw + o, W::kPlaneT, qw[i] * u);
+      store_quads<NB>(s + W::kRe + o, W::kPlaneT, qe[i] * r);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int quad = tid + i * THREADS, t = quad < QUADS ? quad >> 3 : 0;
+    dvu[i] = vdv[i] = 0.0f;
+    qe[i] = -p.e[at * L + t];
+    qw[i] = p.w[at * L + t];
+  }
+  fetch(0);
+  xc.load(rc, state_off, row16, 0);
+  xg.load(rg, state_off, row16, 0);
+  stage(s_K);
+  if (DV > 32) fetch(32);
+
+  for (int v0 = 0; v0 < DV; v0 += 32) {
+    const uint16_t* s = s_K + ((v0 >> 5) & 1) * W::kStage;
+    __syncthreads();  // this step is staged, the one before read out
+    if (v0 + 32 < DV) {
+      nc.load(rc, state_off, row16, v0 + 32);
+      ng.load(rg, state_off, row16, v0 + 32);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 
     // the products with the states: rows of C and G, columns t
+    Parts<3> cp[2];
+    Parts<NB> gp[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      float a[8], b[8];
+      xc.values(i, a);
+      xg.values(i, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) cg += xc[i][e] * xg[i][e];
-      const Parts<3> cp = split_parts<3>(xc[i]);
-      Parts<NB> cb;
+      for (int e = 0; e < 8; ++e) cg += a[e] * b[e];
+      cp[i] = split_parts<3>(a);
+      gp[i] = split_parts<NB>(b);
+    }
 #pragma unroll
-      for (int n = 0; n < NB; ++n) cb.p[n] = cp.p[n];
-      const Parts<NB> gp = split_parts<NB>(xg[i]);
+    for (int j = 0; j < RT; ++j) {
+      const uint16_t* o = s + (16 * j + row) * W::kLdT + 8 * grp;
+      const Parts<NH> h = lds_row8<NH>(o, W::kPlaneT);
+      const Parts<NB> r = lds_row8<NB>(o + W::kRe, W::kPlaneT), u = lds_row8<NB>(o + W::kUw, W::kPlaneT);
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const int o = (16 * j + row) * W::kLdT + 8 * grp;
-        dq[i][j] = mma_parts<3, NH>(cp, lds_row8<NH>(s_H + o, W::kPlaneT), dq[i][j]);
-        dkc[i][j] = mma_parts<NB, NB>(cb, lds_row8<NB>(s_R + o, W::kPlaneT), dkc[i][j]);
-        dkg[i][j] = mma_parts<NB, NB>(gp, lds_row8<NB>(s_U + o, W::kPlaneT), dkg[i][j]);
+      for (int i = 0; i < 2; ++i) {
+        dq[i][j] = mma_parts<3, NH>(cp[i], h, dq[i][j]);
+        dk[i][j] = mma_parts<NB, NB>(first_parts<NB>(cp[i]), r, dk[i][j]);
+        dk[i][j] = mma_parts<NB, NB>(gp[i], u, dk[i][j]);
       }
     }
     // dH U^T and dV U^T
@@ -134,29 +224,34 @@ __global__ __launch_bounds__(2 * DK) void delta_grads_kernel(const DeltaParams p
       if (tile >= NT) break;
       int rt, ct;
       lower_tile(tile, rt, ct);
-      const int oa = (16 * rt + row) * W::kLdT + 8 * grp, ob = (16 * ct + row) * W::kLdT + 8 * grp;
-      const Parts<3> up = lds_row8<3>(s_U + ob, W::kPlaneT);
-      hu[i] = mma_parts<NH, 3>(lds_row8<NH>(s_H + oa, W::kPlaneT), up, hu[i]);
-      Parts<NB> ub;
-#pragma unroll
-      for (int n = 0; n < NB; ++n) ub.p[n] = up.p[n];
-      ru[i] = mma_parts<NB, NB>(lds_row8<NB>(s_R + oa, W::kPlaneT), ub, ru[i]);
+      const uint16_t* a = s + (16 * rt + row) * W::kLdT + 8 * grp;
+      const Parts<3> up = lds_row8<3>(s + W::kU + (16 * ct + row) * W::kLdT + 8 * grp, W::kPlaneT);
+      hu[i] = mma_parts<NH, 3>(lds_row8<NH>(a, W::kPlaneT), up, hu[i]);
+      ru[i] = mma_parts<NB, NB>(lds_row8<NB>(a + W::kR, W::kPlaneT), first_parts<NB>(up), ru[i]);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (v0 + 32 < DV) {
+      stage(s_K + (((v0 >> 5) + 1) & 1) * W::kStage);
+      if (v0 + 64 < DV) fetch(v0 + 64);
+    }
+    xc = nc;
+    xg = ng;
   }
   __syncthreads();  // the staged columns are read out: K and Q take their place
 
-  // row sums of the staged pieces, four lanes a row
+  // row sums of the staged quads, eight lanes a row
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const int piece = tid + i * THREADS;
+    const int quad = tid + i * THREADS;
     float a = dvu[i], b = vdv[i];
-    a += __shfl_xor(a, 1, 64);
-    b += __shfl_xor(b, 1, 64);
-    a += __shfl_xor(a, 2, 64);
-    b += __shfl_xor(b, 2, 64);
-    if (piece < 4 * L && (piece & 3) == 0) {
-      s_dvu[piece >> 2] = a;
-      s_vdv[piece >> 2] = b;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      a += __shfl_xor(a, o, 64);
+      b += __shfl_xor(b, o, 64);
+    }
+    if (quad < QUADS && (quad & 7) == 0) {
+      s_dvu[quad >> 3] = a;
+      s_vdv[quad >> 3] = b;
     }
   }
 #pragma unroll
@@ -202,14 +297,9 @@ __global__ __launch_bounds__(2 * DK) void delta_grads_kernel(const DeltaParams p
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
     const int t = 16 * j + row;
-    const float e = p.e[at * L + t], w = p.w[at * L + t], se = p.scale * e;
+    const float se = p.scale * p.e[at * L + t];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        dq[i][j][r] *= se;
-        dkc[i][j][r] = w * dkg[i][j][r] - e * dkc[i][j][r];
-      }
+    for (int i = 0; i < 2; ++i) dq[i][j] *= se;
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -223,9 +313,9 @@ __global__ __launch_bounds__(2 * DK) void delta_grads_kernel(const DeltaParams p
         const int o = (16 * j + row) * W::kLdS + 32 * s + 8 * grp;
         if (s <= j / 2) dq[i][j] = mma_parts<NP, 3>(kt, lds_row8<3>(s_dP + o, W::kPlaneS), dq[i][j]);
         if (s >= j / 2)
-          dkc[i][j] = mma_parts<NP, NB>(qt, lds_col<NB>(s_dP, W::kLdS, W::kPlaneS, 32 * s + 8 * grp, 4, 16 * j, lane),
-                                        dkc[i][j]);
-        dkc[i][j] = mma_parts<NP, NB>(kt, lds_row8<NB>(s_dA + o, W::kPlaneS), dkc[i][j]);
+          dk[i][j] = mma_parts<NP, NB>(qt, lds_col<NB>(s_dP, W::kLdS, W::kPlaneS, 32 * s + 8 * grp, 4, 16 * j, lane),
+                                        dk[i][j]);
+        dk[i][j] = mma_parts<NP, NB>(kt, lds_row8<NB>(s_dA + o, W::kPlaneS), dk[i][j]);
       }
     }
   }
@@ -248,7 +338,7 @@ __global__ __launch_bounds__(2 * DK) void delta_grads_kernel(const DeltaParams p
       if (t0 + t < p.S) {
         const size_t o = ((size_t)bh * p.S + t0 + t) * DK + k0;
         store4(static_cast<TIn*>(p.dQ) + o, dq[i][j][0], dq[i][j][1], dq[i][j][2], dq[i][j][3]);
-        store4(static_cast<TIn*>(p.dK) + o, dkc[i][j][0], dkc[i][j][1], dkc[i][j][2], dkc[i][j][3]);
+        store4(static_cast<TIn*>(p.dK) + o, dk[i][j][0], dk[i][j][1], dk[i][j][2], dk[i][j][3]);
       }
     }
     dot += __shfl_xor(dot, 16, 64);

@@ -9,57 +9,138 @@
 //   U = T (V - e K C),   H = s (e Q C + P U),   C <- g C + K^T (w U).
 // The accumulator tiles of C, of V - e K C and of U feed straight back as
 // the right operand of the next product: the slot order of two accumulator
-// tiles is matched by how the left operands are read from LDS.
+// tiles is matched by how the left operands are read from LDS.  The next
+// chunk's K, Q, T and P are loaded into registers while this one computes.
 #include "delta_common.h"
 #include "kernels.h"
+#include "pair_store.h"
 
 namespace mlstm {
 namespace {
 
-// LDS of a workgroup: two input tiles (K, Q) and two squares (T, P), as parts.
-template <typename TIn, int DK>
+// LDS of a workgroup: two input tiles (K, Q), two squares (T, P) and e, w.
+template <typename TIn, int DK, int PP>
 struct WalkLds {
-  static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts;
-  static constexpr int kLd = DK + 8, kPlane = L * kLd;
-  static constexpr int kLdS = L + 8, kPlaneS = L * kLdS;
-  static constexpr int kBytes = 2 * (2 * NP * kPlane + 2 * 3 * kPlaneS) + 4 * 2 * L;
+  static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts, NF = square_frags<L>();
+  static constexpr int kPlane = L * DK;
+  static constexpr int kBytes = 2 * (2 * NP * kPlane + NF * (3 + PP) * kFragElems) + 4 * 2 * L;
 };
 
-// acc[rt] += M[rows 16 rt ..][all L] . X for a lower triangular L x L matrix
-// M (LDS planes) and X in parts of 32 rows.
-template <int L, int NX>
-__device__ __forceinline__ void lower_times(const uint16_t* M, int ld, int plane, const Parts<NX> (&x)[L / 32],
-                                            float4_t (&acc)[L / 16], int row, int grp) {
-#pragma unroll
-  for (int rt = 0; rt < L / 16; ++rt)
-#pragma unroll
-    for (int ts = 0; ts <= rt / 2; ++ts)
-      acc[rt] = mma_parts<3, NX>(lds_row44<3>(M + (16 * rt + row) * ld + 32 * ts + 4 * grp, plane), x[ts], acc[rt]);
+// Four values s_x[16 rt + 4 grp ..] of a row vector in LDS.
+__device__ __forceinline__ float4_t row4(const float* x, int rt, int grp) {
+  return *reinterpret_cast<const float4_t*>(x + 16 * rt + 4 * grp);
 }
 
-// acc[rt] += (M^T)[rows 16 rt ..] . X, M lower triangular.
-template <int L, int NX>
-__device__ __forceinline__ void upper_times(const uint16_t* M, int ld, int plane, const Parts<NX> (&x)[L / 32],
-                                            float4_t (&acc)[L / 16], int lane, int grp) {
+// A slice of rows of a row-major matrix of `ld` columns, one lane a column:
+// a buffer resource over `rows` rows from `base` (reads behind them give
+// zero, stores are dropped) and this lane's offset, element (row 4 grp, its
+// column).
+template <typename T>
+struct Slice {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int lane_off, row_bytes;
+  __device__ __forceinline__ Slice(const T* base, int ld, int rows, int off)
+      : rsrc(make_rsrc(base, (uint32_t)rows * ld * (uint32_t)sizeof(T))), lane_off(off * (int)sizeof(T)),
+        row_bytes(ld * (int)sizeof(T)) {}
+};
+
+// The values as they are in memory; they become floats where they are used,
+// so that nothing waits for the loads before.
+template <typename T, int N>
+struct RawTiles {
+  uint32_t x[N][4];
+  __device__ __forceinline__ void load(const Slice<T>& s) {
 #pragma unroll
-  for (int rt = 0; rt < L / 16; ++rt)
+    for (int rt = 0; rt < N; ++rt)
 #pragma unroll
-    for (int ts = rt / 2; ts < L / 32; ++ts)
-      acc[rt] = mma_parts<3, NX>(lds_col<3>(M, ld, plane, 32 * ts + 4 * grp, 16, 16 * rt, lane), x[ts], acc[rt]);
+      for (int r = 0; r < 4; ++r) {
+        const int off = s.lane_off + (16 * rt + r) * s.row_bytes;
+        if constexpr (sizeof(T) == 2) x[rt][r] = __builtin_amdgcn_raw_buffer_load_b16(s.rsrc, off, 0, 0);
+        else x[rt][r] = __builtin_amdgcn_raw_buffer_load_b32(s.rsrc, off, 0, 0);
+      }
+  }
+  __device__ __forceinline__ float4_t tile(int rt) const {
+    float4_t v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = __uint_as_float(sizeof(T) == 2 ? x[rt][r] << 16 : x[rt][r]);
+    return v;
+  }
+};
+
+// Every row is in range: the row offset may be a scalar, which the range
+// check leaves out.
+template <int N>
+__device__ __forceinline__ void store_whole(const Slice<float>& s, const float4_t (&x)[N]) {
+#pragma unroll
+  for (int rt = 0; rt < N; ++rt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[rt][r]), s.rsrc, s.lane_off,
+                                            (16 * rt + r) * s.row_bytes, 0);
+}
+template <int N>
+__device__ __forceinline__ void load_whole(const Slice<float>& s, float4_t (&x)[N]) {
+#pragma unroll
+  for (int rt = 0; rt < N; ++rt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      x[rt][r] = __int_as_float(
+          (int)__builtin_amdgcn_raw_buffer_load_b32(s.rsrc, s.lane_off, (16 * rt + r) * s.row_bytes, 0));
 }
 
-// FWD: H and the final state.  STATES: the state entering every chunk and U,
-// for the backward pass.
-template <typename TIn, int DK, int NW, bool FWD, bool STATES>
-__global__ __launch_bounds__(64 * NW) void delta_walk_kernel(const DeltaParams p) {
-  typedef WalkLds<TIn, DK> W;
+// One accumulator tile in the type of H or V, adjacent lanes paired so that
+// each stores two neighbouring values of a row at once.
+template <typename T>
+__device__ __forceinline__ void store_tile(const Slice<T>& s, int rt, const float4_t& x, float scale, int lane) {
+  const bool odd = lane & 1;
+  const int base = s.lane_off + (odd ? s.row_bytes - (int)sizeof(T) : 0);  // the pair's even column
+#pragma unroll
+  for (int r = 0; r < 4; r += 2) {
+    const float2 v = pair_rows_to_cols(scale * x[r], scale * x[r + 1], odd);
+    const int off = base + (16 * rt + r) * s.row_bytes;
+    if constexpr (sizeof(T) == 2) {
+      __builtin_amdgcn_raw_buffer_store_b32(round_bf16x2(v.x, v.y), s.rsrc, off, 0, 0);
+    } else {
+      const v2i32_t w = {__float_as_int(v.x), __float_as_int(v.y)};
+      __builtin_amdgcn_raw_buffer_store_b64(w, s.rsrc, off, 0, 0);
+    }
+  }
+}
+
+// acc[rt] += a[rt] . b
+template <int N, int NA, int NB>
+__device__ __forceinline__ void rows_times(const Parts<NA> (&a)[N], const Parts<NB>& b, float4_t (&acc)[N]) {
+  constexpr int M = NA > NB ? NA : NB;
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j < M)
+#pragma unroll
+        for (int n = 0; n < N; ++n) acc[n] = mma16b(a[n].p[i], b.p[j], acc[n]);
+}
+
+// w x of one 32-row block as operand parts.
+__device__ __forceinline__ Parts<3> scaled_parts(const float* w, const float4_t* x, int ts, int grp) {
+  float y[8];
+  tiles8(row4(w, 2 * ts, grp) * x[2 * ts], row4(w, 2 * ts + 1, grp) * x[2 * ts + 1], y);
+  return split_parts<3>(y);
+}
+
+// FWD: H (type TH) and the final state.  !FWD: the state entering every chunk
+// and U, for the backward pass.  A bf16 H keeps eight bits: its own products
+// take the state and P in two parts.
+template <typename TIn, typename TH, int DK, int NW, bool FWD>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void delta_walk_kernel(const DeltaParams p) {
+  constexpr int PP = sizeof(TH) == 2 ? 2 : 3;
+  typedef WalkLds<TIn, DK, FWD ? PP : 0> W;
   constexpr int L = W::L, NP = W::NP, RT = L / 16, TS = L / 32, KT = DK / 16, THREADS = 64 * NW;
   __shared__ uint4 smem[W::kBytes / 16];
   uint16_t* s_K = reinterpret_cast<uint16_t*>(smem);
   uint16_t* s_Q = s_K + NP * W::kPlane;
   uint16_t* s_T = s_Q + NP * W::kPlane;
-  uint16_t* s_P = s_T + 3 * W::kPlaneS;
-  float* s_e = reinterpret_cast<float*>(s_P + 3 * W::kPlaneS);
+  uint16_t* s_P = s_T + W::NF * 3 * kFragElems;
+  float* s_e = reinterpret_cast<float*>(s_P + (FWD ? W::NF * PP * kFragElems : 0));
   float* s_w = s_e + L;
 
   // slices of one head share an XCD's L2 where the head count is a multiple of 8
@@ -69,60 +150,93 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(const DeltaParams p
   const int col = (slice * NW + wave) * 16 + row;
   const TIn* K = static_cast<const TIn*>(p.K) + (size_t)bh * p.S * DK;
   const TIn* Q = static_cast<const TIn*>(p.Q) + (size_t)bh * p.S * DK;
-  const TIn* V = static_cast<const TIn*>(p.V) + (size_t)bh * p.S * p.DV + col;
+  const TIn* V = static_cast<const TIn*>(p.V) + (size_t)bh * p.S * p.DV;
+  constexpr int kSquare = W::NF * 3 * kFragElems;
+  int io_off = 4 * grp * p.DV + col;  // rows 16 rt + 4 grp + r of its column
+  int row_seed = tile_row_seed<DK>(row, grp), col_seed = tile_col_seed<DK>(grp, lane);
 
   float4_t C[KT];
 #pragma unroll
-  for (int k = 0; k < KT; ++k)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      C[k][r] = p.C0 ? p.C0[((size_t)bh * DK + 16 * k + 4 * grp + r) * p.DV + col] : 0.0f;
+  for (int k = 0; k < KT; ++k) C[k] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.C0) load_whole(Slice<float>(p.C0 + (size_t)bh * DK * p.DV, p.DV, DK, io_off), C);
+
+  TileStage<TIn, DK, THREADS> gk, gq;
+  SquareStage<L, 3, THREADS> gt;
+  SquareStage<L, PP, THREADS> gp;
+  float ge = 0.0f;
+  auto fetch = [&](int c) {
+    const size_t at = (size_t)bh * p.Nc + c;
+    const int rows = p.S - c * L < L ? p.S - c * L : L;
+    gk.load(K + (size_t)c * L * DK, rows, tid);
+    if constexpr (FWD) gq.load(Q + (size_t)c * L * DK, rows, tid);
+    gt.load(p.T + at * kSquare, tid);
+    if constexpr (FWD) gp.load(p.P + at * kSquare, tid);
+    if (tid < 2 * L) ge = tid < L ? p.e[at * L + tid] : p.w[at * L + tid - L];
+  };
+  if (p.Nc) fetch(0);
 
   for (int c = 0; c < p.Nc; ++c) {
     const int t0 = c * L;
     const size_t at = (size_t)bh * p.Nc + c;
-    // this lane's values of V: rows 16 rt + 4 grp + r of its column
-    float4_t v[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = t0 + 16 * rt + 4 * grp + r;
-        v[rt][r] = t < p.S ? load1(V + (size_t)t * p.DV) : 0.0f;
-      }
+    keep_in_loop(row_seed);
+    keep_in_loop(col_seed);
+    keep_in_loop(io_off);
     __syncthreads();  // the chunk before is read out
-    stage_rows<TIn, L, DK>(s_K, W::kLd, W::kPlane, K, t0, p.S, tid, THREADS);
-    if constexpr (FWD) stage_rows<TIn, L, DK>(s_Q, W::kLd, W::kPlane, Q, t0, p.S, tid, THREADS);
-    stage_square<L>(s_T, W::kLdS, W::kPlaneS, p.T + at * L * L, tid, THREADS);
-    if constexpr (FWD) stage_square<L>(s_P, W::kLdS, W::kPlaneS, p.P + at * L * L, tid, THREADS);
-    if (tid < L) {
-      s_e[tid] = p.e[at * L + tid];
-      s_w[tid] = p.w[at * L + tid];
-    }
+    gk.store(s_K, W::kPlane, tid);
+    if constexpr (FWD) gq.store(s_Q, W::kPlane, tid);
+    gt.store(s_T, tid);
+    if constexpr (FWD) gp.store(s_P, tid);
+    if (tid < 2 * L) s_e[tid] = ge;
     __syncthreads();
+    if (c + 1 < p.Nc) fetch(c + 1);
+    RawTiles<TIn, RT> v;
+    const int rows = p.S - t0 < L ? p.S - t0 : L;
+    v.load(Slice<TIn>(V + (size_t)t0 * p.DV, p.DV, rows, io_off));
+    __builtin_amdgcn_sched_barrier(0);  // all loads are on their way
 
-    if constexpr (STATES) {
-      float* Cs = p.C_states + at * DK * p.DV + col;
-#pragma unroll
-      for (int k = 0; k < KT; ++k)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) Cs[(size_t)(16 * k + 4 * grp + r) * p.DV] = C[k][r];
+    if constexpr (!FWD) {
+      store_whole(Slice<float>(p.C_states + at * DK * p.DV, p.DV, DK, io_off), C);
     }
 
-    // K C and Q C
+    // K C and Q C: a step is one 32-row block of the state against K's rows,
+    // the next one against Q's.  A block that has become operand parts is
+    // scaled by g on the way.
+    const float g = s_e[L - 1];
     float4_t kc[RT], qc[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) kc[rt] = qc[rt] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int ks = 0; ks < DK / 32; ++ks) {
+    {
+      Parts<NP> f[RT], next[RT];
       float x[8];
-      tiles8(C[2 * ks], C[2 * ks + 1], x);
-      const Parts<3> cp = split_parts<3>(x);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int off = (16 * rt + row) * W::kLd + 32 * ks + 4 * grp;
-        kc[rt] = mma_parts<NP, 3>(lds_row44<NP>(s_K + off, W::kPlane), cp, kc[rt]);
-        if constexpr (FWD) qc[rt] = mma_parts<NP, 3>(lds_row44<NP>(s_Q + off, W::kPlane), cp, qc[rt]);
+      for (int rt = 0; rt < RT; ++rt) f[rt] = tile_row<NP, DK>(s_K, W::kPlane, row_seed, rt, 0);
+      tiles8(C[0], C[1], x);
+      Parts<3> cp = split_parts<3>(x), cn = cp;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int ks = 0; ks < DK / 32; ++ks) {
+        C[2 * ks] *= g;
+        C[2 * ks + 1] *= g;
+        if constexpr (FWD) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) next[rt] = tile_row<NP, DK>(s_Q, W::kPlane, row_seed, rt, ks);
+          rows_times(f, cp, kc);
+          end_step<2 * NP * RT, RT * mma_count<NP, 3>(), 1>();
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) f[rt] = next[rt];
+        }
+        if (ks + 1 < DK / 32) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) next[rt] = tile_row<NP, DK>(s_K, W::kPlane, row_seed, rt, ks + 1);
+          tiles8(C[2 * ks + 2], C[2 * ks + 3], x);
+          cn = split_parts<3>(x);
+        }
+        if constexpr (FWD) rows_times(f, first_parts<PP>(cp), qc);
+        else rows_times(f, cp, kc);
+        if (ks + 1 < DK / 32) end_step<2 * NP * RT, RT * (FWD ? mma_count<NP, PP>() : mma_count<NP, 3>()), FWD ? 6 : 4>();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) f[rt] = next[rt];
+        cp = cn;
       }
     }
 
@@ -133,93 +247,50 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(const DeltaParams p
 #pragma unroll
       for (int ts = 0; ts < TS; ++ts) {
         float x[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 e = *reinterpret_cast<const float4*>(s_e + 32 * ts + 16 * h + 4 * grp);
-          const float ev[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[4 * h + r] = v[2 * ts + h][r] - ev[r] * kc[2 * ts + h][r];
-        }
+        tiles8(v.tile(2 * ts) - row4(s_e, 2 * ts, grp) * kc[2 * ts],
+               v.tile(2 * ts + 1) - row4(s_e, 2 * ts + 1, grp) * kc[2 * ts + 1], x);
         xp[ts] = split_parts<3>(x);
       }
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) u[rt] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-      lower_times<L, 3>(s_T, W::kLdS, W::kPlaneS, xp, u, row, grp);
+      __builtin_amdgcn_sched_barrier(0);
+      square_times<L, false, 3, 3, 1>(s_T, xp, u, lane, [&](int i) {
+        if (FWD && i < RT) qc[i] *= row4(s_e, i, grp);
+      });
     }
-    if constexpr (STATES) {
-      float* U = p.U + at * L * p.DV + col;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) U[(size_t)(16 * rt + 4 * grp + r) * p.DV] = u[rt][r];
-    }
+    if constexpr (!FWD) store_whole(Slice<float>(p.U + at * L * p.DV, p.DV, L, io_off), u);
 
-    // H = s (e Q C + P U)
+    // H = s (e Q C + P U), the parts of w U on the way
+    Parts<3> wp[TS];
     if constexpr (FWD) {
-      Parts<3> up[TS];
+      Parts<PP> up[TS];
 #pragma unroll
       for (int ts = 0; ts < TS; ++ts) {
         float x[8];
         tiles8(u[2 * ts], u[2 * ts + 1], x);
-        up[ts] = split_parts<3>(x);
+        up[ts] = split_parts<PP>(x);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      square_times<L, false, PP, PP, 6>(s_P, up, qc, lane, [&](int i) {
+        if (i < TS) wp[i] = scaled_parts(s_w, u, i, grp);
+      });
+    } else {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const float4 e = *reinterpret_cast<const float4*>(s_e + 16 * rt + 4 * grp);
-        qc[rt][0] *= e.x;
-        qc[rt][1] *= e.y;
-        qc[rt][2] *= e.z;
-        qc[rt][3] *= e.w;
-      }
-      lower_times<L, 3>(s_P, W::kLdS, W::kPlaneS, up, qc, row, grp);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = t0 + 16 * rt + 4 * grp + r;
-          if (t < p.S) {
-            const size_t o = ((size_t)bh * p.S + t) * p.DV + col;
-            if (p.h_bf16) store1(static_cast<bf16_t*>(p.H) + o, p.scale * qc[rt][r]);
-            else store1(static_cast<float*>(p.H) + o, p.scale * qc[rt][r]);
-          }
-        }
+      for (int ts = 0; ts < TS; ++ts) wp[ts] = scaled_parts(s_w, u, ts, grp);
+      __builtin_amdgcn_sched_barrier(0);
     }
 
-    // C <- g C + K^T (w U)
-    {
-      Parts<3> wp[TS];
+    // C <- g C + K^T (w U), the stores of H on the way
+    const Slice<TH> out(FWD ? static_cast<TH*>(p.H) + ((size_t)bh * p.S + t0) * p.DV : nullptr, p.DV, rows, io_off);
 #pragma unroll
-      for (int ts = 0; ts < TS; ++ts) {
-        float x[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 w = *reinterpret_cast<const float4*>(s_w + 32 * ts + 16 * h + 4 * grp);
-          const float wv[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[4 * h + r] = wv[r] * u[2 * ts + h][r];
-        }
-        wp[ts] = split_parts<3>(x);
-      }
-      const float g = s_e[L - 1];
-#pragma unroll
-      for (int k = 0; k < KT; ++k) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) C[k][r] *= g;
-#pragma unroll
-        for (int ts = 0; ts < TS; ++ts)
-          C[k] = mma_parts<NP, 3>(lds_col<NP>(s_K, W::kLd, W::kPlane, 32 * ts + 4 * grp, 16, 16 * k, lane), wp[ts],
-                                  C[k]);
-      }
-    }
+    for (int ts = 0; ts < TS; ++ts)
+      tile_cols_times<NP, DK, 3>(s_K, W::kPlane, col_seed, ts, wp[ts], C, [&](int i) {
+        const int rt = ts * (DK / 32) + i;
+        if (FWD && rt < RT) store_tile(out, rt, qc[rt], p.scale, lane);
+      });
   }
 
-  if (p.C_out) {
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        p.C_out[((size_t)bh * DK + 16 * k + 4 * grp + r) * p.DV + col] = C[k][r];
-  }
+  if (p.C_out) store_whole(Slice<float>(p.C_out + (size_t)bh * DK * p.DV, p.DV, DK, io_off), C);
 }
 
 // The backward walk, last chunk first.  G is the gradient of the state
@@ -229,16 +300,16 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(const DeltaParams p
 // It writes G of every chunk and dV for the gradient kernel, and per column
 // slice the chunk's sum of w_t u_t . (K G)_t, one half of <C, G> behind the
 // chunk that the gate gradient needs.
-template <typename TIn, int DK, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_walk_back_kernel(const DeltaParams p) {
-  typedef WalkLds<TIn, DK> W;
+template <typename TIn, typename TH, int DK, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void delta_walk_back_kernel(const DeltaParams p) {
+  typedef WalkLds<TIn, DK, 3> W;
   constexpr int L = W::L, NP = W::NP, RT = L / 16, TS = L / 32, KT = DK / 16, THREADS = 64 * NW;
   __shared__ uint4 smem[W::kBytes / 16];
   uint16_t* s_K = reinterpret_cast<uint16_t*>(smem);
   uint16_t* s_Q = s_K + NP * W::kPlane;
   uint16_t* s_T = s_Q + NP * W::kPlane;
-  uint16_t* s_P = s_T + 3 * W::kPlaneS;
-  float* s_e = reinterpret_cast<float*>(s_P + 3 * W::kPlaneS);
+  uint16_t* s_P = s_T + W::NF * 3 * kFragElems;
+  float* s_e = reinterpret_cast<float*>(s_P + W::NF * 3 * kFragElems);
   float* s_w = s_e + L;
 
   const int bh = blockIdx.x % p.BH, slice = blockIdx.x / p.BH;
@@ -247,188 +318,180 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_back_kernel(const DeltaPar
   const int col = (slice * NW + wave) * 16 + row;
   const TIn* K = static_cast<const TIn*>(p.K) + (size_t)bh * p.S * DK;
   const TIn* Q = static_cast<const TIn*>(p.Q) + (size_t)bh * p.S * DK;
+  const TH* dH = static_cast<const TH*>(p.dH) + (size_t)bh * p.S * p.DV;
+  constexpr int kSquare = W::NF * 3 * kFragElems;
+  int io_off = 4 * grp * p.DV + col;  // rows 16 rt + 4 grp + r of its column
+  int row_seed = tile_row_seed<DK>(row, grp), col_seed = tile_col_seed<DK>(grp, lane);
 
   float4_t G[KT];
 #pragma unroll
-  for (int k = 0; k < KT; ++k)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      G[k][r] = p.dC_out ? p.dC_out[((size_t)bh * DK + 16 * k + 4 * grp + r) * p.DV + col] : 0.0f;
+  for (int k = 0; k < KT; ++k) G[k] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.dC_out) load_whole(Slice<float>(p.dC_out + (size_t)bh * DK * p.DV, p.DV, DK, io_off), G);
+
+  TileStage<TIn, DK, THREADS> gk, gq;
+  SquareStage<L, 3, THREADS> gt, gp;
+  float ge = 0.0f;
+  auto fetch = [&](int c) {
+    const size_t at = (size_t)bh * p.Nc + c;
+    const int rows = p.S - c * L < L ? p.S - c * L : L;
+    gk.load(K + (size_t)c * L * DK, rows, tid);
+    gq.load(Q + (size_t)c * L * DK, rows, tid);
+    gt.load(p.Tt + at * kSquare, tid);
+    gp.load(p.P + at * kSquare, tid);
+    if (tid < 2 * L) ge = tid < L ? p.e[at * L + tid] : p.w[at * L + tid - L];
+  };
+  if (p.Nc) fetch(p.Nc - 1);
 
   for (int c = p.Nc - 1; c >= 0; --c) {
     const int t0 = c * L;
     const size_t at = (size_t)bh * p.Nc + c;
-    float4_t dh[RT], u[RT];
-    const float* U = p.U + at * L * p.DV + col;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * rt + 4 * grp + r;
-        float x = 0.0f;
-        if (t0 + t < p.S) {
-          const size_t o = ((size_t)bh * p.S + t0 + t) * p.DV + col;
-          x = p.h_bf16 ? load1(static_cast<const bf16_t*>(p.dH) + o) : load1(static_cast<const float*>(p.dH) + o);
-        }
-        dh[rt][r] = x;
-        u[rt][r] = U[(size_t)t * p.DV];
-      }
+    keep_in_loop(row_seed);
+    keep_in_loop(col_seed);
+    keep_in_loop(io_off);
+    __syncthreads();  // the chunk before is read out
+    gk.store(s_K, W::kPlane, tid);
+    gq.store(s_Q, W::kPlane, tid);
+    gt.store(s_T, tid);
+    gp.store(s_P, tid);
+    if (tid < 2 * L) s_e[tid] = ge;
     __syncthreads();
-    stage_rows<TIn, L, DK>(s_K, W::kLd, W::kPlane, K, t0, p.S, tid, THREADS);
-    stage_rows<TIn, L, DK>(s_Q, W::kLd, W::kPlane, Q, t0, p.S, tid, THREADS);
-    stage_square<L>(s_T, W::kLdS, W::kPlaneS, p.T + at * L * L, tid, THREADS);
-    stage_square<L>(s_P, W::kLdS, W::kPlaneS, p.P + at * L * L, tid, THREADS);
-    if (tid < L) {
-      s_e[tid] = p.e[at * L + tid];
-      s_w[tid] = p.w[at * L + tid];
-    }
-    __syncthreads();
+    if (c > 0) fetch(c - 1);
+    float4_t u[RT], dh[RT];
+    RawTiles<TH, RT> raw;
+    const int rows = p.S - t0 < L ? p.S - t0 : L;
+    load_whole(Slice<float>(p.U + at * L * p.DV, p.DV, L, io_off), u);
+    raw.load(Slice<TH>(dH + (size_t)t0 * p.DV, p.DV, rows, io_off));
+    __builtin_amdgcn_sched_barrier(0);  // all loads are on their way
+    store_whole(Slice<float>(p.G_states + at * DK * p.DV, p.DV, DK, io_off), G);
 
-    float* Gs = p.G_states + at * DK * p.DV + col;
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) Gs[(size_t)(16 * k + 4 * grp + r) * p.DV] = G[k][r];
-
-    // K G
+    // w K G, and its product with u; blocks of G are scaled by g on the way
+    const float g = s_e[L - 1];
     float4_t kg[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) kg[rt] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int ks = 0; ks < DK / 32; ++ks) {
+    {
+      Parts<NP> f[RT], next[RT];
       float x[8];
-      tiles8(G[2 * ks], G[2 * ks + 1], x);
-      const Parts<3> gp = split_parts<3>(x);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        kg[rt] = mma_parts<NP, 3>(lds_row44<NP>(s_K + (16 * rt + row) * W::kLd + 32 * ks + 4 * grp, W::kPlane), gp,
-                                  kg[rt]);
+      for (int rt = 0; rt < RT; ++rt) f[rt] = tile_row<NP, DK>(s_K, W::kPlane, row_seed, rt, 0);
+      tiles8(G[0], G[1], x);
+      Parts<3> gs = split_parts<3>(x), gn = gs;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int ks = 0; ks < DK / 32; ++ks) {
+        G[2 * ks] *= g;
+        G[2 * ks + 1] *= g;
+        if (ks + 1 < DK / 32) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) next[rt] = tile_row<NP, DK>(s_K, W::kPlane, row_seed, rt, ks + 1);
+          tiles8(G[2 * ks + 2], G[2 * ks + 3], x);
+          gn = split_parts<3>(x);
+        }
+        rows_times(f, gs, kg);
+        if (ks + 1 < DK / 32) end_step<2 * NP * RT, RT * mma_count<NP, 3>(), 5>();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) f[rt] = next[rt];
+        gs = gn;
+      }
+    }
+    float anchor = 0.0f;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      kg[rt] *= row4(s_w, rt, grp);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) anchor += kg[rt][r] * u[rt][r];
+      dh[rt] = p.scale * raw.tile(rt);
     }
 
-    // w K G, its product with u, and s dH as parts
-    float anchor = 0.0f;
-    Parts<3> hp[TS];
+    // dU
+    Parts<3> xp[TS], hp[TS];
 #pragma unroll
     for (int ts = 0; ts < TS; ++ts) {
       float x[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 w = *reinterpret_cast<const float4*>(s_w + 32 * ts + 16 * h + 4 * grp);
-        const float wv[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float4_t& k4 = kg[2 * ts + h];
-          k4[r] *= wv[r];
-          anchor += k4[r] * u[2 * ts + h][r];
-          x[4 * h + r] = p.scale * dh[2 * ts + h][r];
-        }
-      }
-      hp[ts] = split_parts<3>(x);
+      tiles8(dh[2 * ts], dh[2 * ts + 1], x);
+      xp[ts] = split_parts<3>(x);
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) anchor += __shfl_xor(anchor, o, 64);
-    if (lane == 0) p.anchor[at * (p.DV / 16) + slice * NW + wave] = anchor;
-    upper_times<L, 3>(s_P, W::kLdS, W::kPlaneS, hp, kg, lane, grp);  // dU
+    __builtin_amdgcn_sched_barrier(0);
+    square_times<L, true, 3, 3, 3>(s_P, xp, kg, lane, [&](int i) {
+      if (i < TS) hp[i] = scaled_parts(s_e, dh, i, grp);
+    });
 
     // dV = T^T dU
     float4_t dv[RT];
-    {
-      Parts<3> xp[TS];
 #pragma unroll
-      for (int ts = 0; ts < TS; ++ts) {
-        float x[8];
-        tiles8(kg[2 * ts], kg[2 * ts + 1], x);
-        xp[ts] = split_parts<3>(x);
-      }
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) dv[rt] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-      upper_times<L, 3>(s_T, W::kLdS, W::kPlaneS, xp, dv, lane, grp);
+    for (int ts = 0; ts < TS; ++ts) {
+      float x[8];
+      tiles8(kg[2 * ts], kg[2 * ts + 1], x);
+      xp[ts] = split_parts<3>(x);
     }
-    float* R = p.R + at * L * p.DV + col;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * rt + 4 * grp + r;
-        R[(size_t)t * p.DV] = dv[rt][r];
-        if (t0 + t < p.S) store1(static_cast<TIn*>(p.dV) + ((size_t)bh * p.S + t0 + t) * p.DV + col, dv[rt][r]);
-      }
+    for (int rt = 0; rt < RT; ++rt) dv[rt] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    __builtin_amdgcn_sched_barrier(0);
+    square_times<L, true, 3, 3, 1>(s_T, xp, dv, lane);
 
-    // G <- g G + Q^T (s e dH) - K^T (e dV)
-    {
-      Parts<3> hq[TS], vk[TS];
+    // G <- g G + Q^T (s e dH) - K^T (e dV), the stores of dV and the parts of
+    // -e dV on the way
+    const Slice<TIn> out(static_cast<TIn*>(p.dV) + ((size_t)bh * p.S + t0) * p.DV, p.DV, rows, io_off);
+    const Slice<float> keep(p.R + at * L * p.DV, p.DV, L, io_off);
 #pragma unroll
-      for (int ts = 0; ts < TS; ++ts) {
-        float x[8], y[8];
+    for (int ts = 0; ts < TS; ++ts)
+      tile_cols_times<NP, DK, 3>(s_Q, W::kPlane, col_seed, ts, hp[ts], G, [&](int i) {
+        const int rt = ts * (DK / 32) + i;
+        if (rt < RT) {
+          store_tile(out, rt, dv[rt], 1.0f, lane);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 e = *reinterpret_cast<const float4*>(s_e + 32 * ts + 16 * h + 4 * grp);
-          const float ev[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x[4 * h + r] = p.scale * ev[r] * dh[2 * ts + h][r];
-            y[4 * h + r] = -ev[r] * dv[2 * ts + h][r];
-          }
+          for (int r = 0; r < 4; ++r)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dv[rt][r]), keep.rsrc, keep.lane_off,
+                                                  (16 * rt + r) * keep.row_bytes, 0);
         }
-        hq[ts] = split_parts<3>(x);
-        vk[ts] = split_parts<3>(y);
-      }
-      const float g = s_e[L - 1];
+        if (i == DK / 32 - 1) {
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) G[k][r] *= g;
-#pragma unroll
-        for (int ts = 0; ts < TS; ++ts) {
-          G[k] = mma_parts<NP, 3>(lds_col<NP>(s_Q, W::kLd, W::kPlane, 32 * ts + 4 * grp, 16, 16 * k, lane), hq[ts],
-                                  G[k]);
-          G[k] = mma_parts<NP, 3>(lds_col<NP>(s_K, W::kLd, W::kPlane, 32 * ts + 4 * grp, 16, 16 * k, lane), vk[ts],
-                                  G[k]);
+          for (int h = 0; h < 2; ++h) dv[2 * ts + h] = -dv[2 * ts + h];
+          xp[ts] = scaled_parts(s_e, dv, ts, grp);
         }
-      }
-    }
+      });
+#pragma unroll
+    for (int ts = 0; ts < TS; ++ts) tile_cols_times<NP, DK, 2>(s_K, W::kPlane, col_seed, ts, xp[ts], G);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) anchor += __shfl_xor(anchor, o, 64);
+    if (lane == 0) p.anchor[at * (p.DV / 16) + slice * NW + wave] = anchor;
   }
 
-  if (p.dC0) {
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        p.dC0[((size_t)bh * DK + 16 * k + 4 * grp + r) * p.DV + col] = G[k][r];
-  }
+  if (p.dC0) store_whole(Slice<float>(p.dC0 + (size_t)bh * DK * p.DV, p.DV, DK, io_off), G);
 }
 
-// Waves a workgroup, sixteen columns each: as many as still leave a
-// workgroup for every CU, since they share the staging of K, Q, T and P.
-int walk_waves(int BH, int DV) {
-  if (DV % 128 == 0 && (long long)BH * (DV / 128) >= 256) return 8;
-  if ((long long)BH * (DV / 64) >= 256) return 4;
-  return 2;
-}
-
-template <typename TIn, int DK, int NW>
+template <typename TIn, typename TH, int DK, int NW>
 hipError_t launch_nw(const DeltaParams& p, DeltaWalk what, hipStream_t stream) {
   const dim3 grid((unsigned)((long long)p.BH * (p.DV / (16 * NW)))), block(64 * NW);
   switch (what) {
     case DeltaWalk::kForward:
-      hipLaunchKernelGGL((delta_walk_kernel<TIn, DK, NW, true, false>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((delta_walk_kernel<TIn, TH, DK, NW, true>), grid, block, 0, stream, p);
       break;
     case DeltaWalk::kStates:
-      hipLaunchKernelGGL((delta_walk_kernel<TIn, DK, NW, false, true>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((delta_walk_kernel<TIn, float, DK, NW, false>), grid, block, 0, stream, p);
       break;
     case DeltaWalk::kBack:
-      hipLaunchKernelGGL((delta_walk_back_kernel<TIn, DK, NW>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((delta_walk_back_kernel<TIn, TH, DK, NW>), grid, block, 0, stream, p);
       break;
   }
   return hipGetLastError();
 }
 
-template <typename TIn, int DK>
+// Waves a workgroup, sixteen columns each: eight where that still leaves a
+// workgroup for every CU, since they share the staging of K, Q, T and P.
+template <typename TIn, typename TH, int DK>
 hipError_t launch_dk(const DeltaParams& p, DeltaWalk what, hipStream_t stream) {
-  switch (walk_waves(p.BH, p.DV)) {
-    case 8: return launch_nw<TIn, DK, 8>(p, what, stream);
-    case 4: return launch_nw<TIn, DK, 4>(p, what, stream);
-    default: return launch_nw<TIn, DK, 2>(p, what, stream);
+  if (p.DV % 128 == 0 && (long long)p.BH * (p.DV / 128) >= 256) return launch_nw<TIn, TH, DK, 8>(p, what, stream);
+  return launch_nw<TIn, TH, DK, 4>(p, what, stream);
+}
+
+template <typename TIn, typename TH>
+hipError_t launch_types(const DeltaParams& p, DeltaWalk what, hipStream_t stream) {
+  switch (p.DK) {
+    case 64: return launch_dk<TIn, TH, 64>(p, what, stream);
+    case 128: return launch_dk<TIn, TH, 128>(p, what, stream);
+    case 256: return launch_dk<TIn, TH, 256>(p, what, stream);
+    default: return hipErrorInvalidValue;
   }
 }
 
@@ -436,12 +499,9 @@ hipError_t launch_dk(const DeltaParams& p, DeltaWalk what, hipStream_t stream) {
 
 hipError_t launch_delta_walk(const DeltaParams& p, DeltaWalk what, hipStream_t stream) {
   if (p.DV <= 0 || p.DV % 64 != 0) return hipErrorInvalidValue;
-  switch (p.DK) {
-    case 64: return p.qkv_bf16 ? launch_dk<bf16_t, 64>(p, what, stream) : launch_dk<float, 64>(p, what, stream);
-    case 128: return p.qkv_bf16 ? launch_dk<bf16_t, 128>(p, what, stream) : launch_dk<float, 128>(p, what, stream);
-    case 256: return p.qkv_bf16 ? launch_dk<bf16_t, 256>(p, what, stream) : launch_dk<float, 256>(p, what, stream);
-    default: return hipErrorInvalidValue;
-  }
+  if (p.qkv_bf16)
+    return p.h_bf16 ? launch_types<bf16_t, bf16_t>(p, what, stream) : launch_types<bf16_t, float>(p, what, stream);
+  return p.h_bf16 ? launch_types<float, bf16_t>(p, what, stream) : launch_types<float, float>(p, what, stream);
 }
 
 }  // namespace mlstm

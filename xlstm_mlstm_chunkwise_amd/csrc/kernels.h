@@ -270,8 +270,9 @@ struct DeltaParams {
   float* d_f;
   float* dC0;  // may be null
   // workspace
-  float* T;      // (at, L, L)
-  float* P;      // (at, L, L)
+  uint16_t* T;   // (at, square) fragments of T and P, or of their transposes
+  uint16_t* P;   // (backward walk): delta_common.h has the order
+  uint16_t* Tt;  // (at, square) fragments of T^T (backward)
   double* bsum;  // (at, L) sum of log a within the chunk
   float* e;      // (at, L) e^bsum
   float* w;      // (at, L) e^(bsum of the last row - bsum)
@@ -285,8 +286,12 @@ struct DeltaParams {
   int qkv_bf16, h_bf16;
 };
 
+// Bytes of one L x L triangle in operand order: fragments of 16 x 32 values in
+// three bf16 planes.
+constexpr size_t delta_square_bytes(int L) { return (size_t)(L == 64 ? 6 : 2) * 3 * 1024; }
+
 enum class DeltaWalk { kForward, kStates, kBack };
-hipError_t launch_delta_prep(const DeltaParams& p, hipStream_t stream);
+hipError_t launch_delta_prep(const DeltaParams& p, bool back, hipStream_t stream);
 hipError_t launch_delta_walk(const DeltaParams& p, DeltaWalk what, hipStream_t stream);
 hipError_t launch_delta_grads(const DeltaParams& p, hipStream_t stream);
 
