@@ -234,11 +234,14 @@ __device__ __forceinline__ void stage_rows(uint16_t* dst, int ld, int plane, con
 // from sixteen rows at once (the row operand), and 32 consecutive bytes from
 // eight rows at once (the transposing read).  Rotating the row number's bits
 // by one gives sixteen different slots to the first and different pairs of
-// slots to the second.  (A row of 64 values spans half the banks, so there
-// two rows share a swizzle.)
+// slots to the second.  (A row of 64 values spans half the banks and a row of
+// 32 a quarter, so there two or four rows share a swizzle.)
 template <int DK>
 __device__ __forceinline__ int tile_swizzle(int r) {
-  if constexpr (DK == 64) {
+  if constexpr (DK == 32) {
+    const int x = (r >> 2) & 3;
+    return ((x << 1) | (x >> 1)) & 3;
+  } else if constexpr (DK == 64) {
     const int x = (r >> 1) & 7;
     return ((x << 1) | (x >> 2)) & 7;
   } else {

@@ -293,6 +293,8 @@ constexpr size_t delta_square_bytes(int L) { return (size_t)(L == 64 ? 6 : 2) * 
 enum class DeltaWalk { kForward, kStates, kBack };
 hipError_t launch_delta_prep(const DeltaParams& p, bool back, hipStream_t stream);
 hipError_t launch_delta_walk(const DeltaParams& p, DeltaWalk what, hipStream_t stream);
+// The form of the walks for few heads: launch_delta_walk chooses it.
+hipError_t launch_delta_split(const DeltaParams& p, DeltaWalk what, hipStream_t stream);
 hipError_t launch_delta_grads(const DeltaParams& p, hipStream_t stream);
 
 struct DeltaStepParams {
