@@ -12,7 +12,7 @@
 // sum_t w_t u_t . (K G)_t formed afresh for every chunk: one running sum over
 // the whole sequence would add up the roundings of all tokens behind t.
 //
-// One workgroup per chunk, DHQK / 32 waves: wave i owns rows 32 i .. 32 i + 31
+// One workgroup per chunk, four or eight waves: each owns one or two row tiles
 // of C and G, which it reads from memory straight into its operands, and
 // forms dQ^T and dK^T for them; the 64 x 64 products are spread over the
 // waves.  dH, U and dV go through LDS in steps of 32 value columns, two
@@ -36,23 +36,28 @@ template <typename TIn, typename TH, int DK>
 struct GradLds {
   static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts, NH = DeltaIn<TH>::kParts;
   static constexpr int NB = NP == 1 ? 2 : 3;  // parts of the terms of dK alone, which is stored as TIn
+  // row tiles of the states a wave, waves, and buffers of a step.  At 256 rows
+  // a workgroup fills a CU's registers; smaller heads leave room for two
+  // workgroups, which hide each other's waits better than a second buffer.
+  static constexpr int KPW = DK == 64 ? 1 : 2, NW = DK / (16 * KPW), BUFS = DK == 256 ? 2 : 1;
   static constexpr int kLdT = 40, kPlaneT = L * kLdT;  // 32 value columns
   // planes of a step: dH, U, dV, w U, -e dV
   static constexpr int kU = NH * kPlaneT, kR = kU + 3 * kPlaneT, kUw = kR + NB * kPlaneT, kRe = kUw + NB * kPlaneT;
   static constexpr int kStage = kRe + NB * kPlaneT;
-  // behind the last step, in the same space: K, Q, dP and dA + dA^T
+  // behind the last step, in the same space: K, then Q, dP and dA + dA^T
   static constexpr int kLd = DK + 8, kPlane = L * kLd, kLdS = L + 8, kPlaneS = L * kLdS;
-  static constexpr int kAfter = 2 * NP * kPlane + 2 * 3 * kPlaneS;
-  static constexpr int kBytes = 2 * (2 * kStage > kAfter ? 2 * kStage : kAfter);
+  static constexpr int kAfter = NP * kPlane + (3 + NB) * kPlaneS;
+  static constexpr int kBytes = 2 * (BUFS * kStage > kAfter ? BUFS * kStage : kAfter);
 };
 
 // This lane's part of 32 value columns of sixteen rows of C or G: eight
 // consecutive values.
+template <int KPW>
 struct StateRows {
-  words4_t x[2][2];
+  words4_t x[KPW][2];
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int lane_off, int row16, int v0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < KPW; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         x[i][h] = __builtin_bit_cast(
@@ -97,19 +102,18 @@ __device__ __forceinline__ void store_quads(uint16_t* p, int plane, const float4
 }
 
 template <typename TIn, typename TH, int DK>
-__global__ __launch_bounds__(2 * DK) __attribute__((amdgpu_waves_per_eu(DK == 256 ? 2 : 1, DK == 256 ? 2 : 4))) void
+__global__ __launch_bounds__((64 * GradLds<TIn, TH, DK>::NW)) __attribute__((amdgpu_waves_per_eu(2))) void
 delta_grads_kernel(const DeltaParams p) {
   typedef GradLds<TIn, TH, DK> W;
-  constexpr int L = W::L, NP = W::NP, NH = W::NH, NB = W::NB, NW = DK / 32, THREADS = 64 * NW;
+  constexpr int L = W::L, NP = W::NP, NH = W::NH, NB = W::NB, KPW = W::KPW, NW = W::NW, THREADS = 64 * NW;
   constexpr int RT = L / 16, NT = RT * (RT + 1) / 2, TPW = (NT + NW - 1) / NW;
   constexpr int QUADS = 8 * L, ROWS = (QUADS + THREADS - 1) / THREADS;
   __shared__ uint4 smem[W::kBytes / 16];
   __shared__ float s_red[NW][L];
   __shared__ float s_dvu[L], s_vdv[L], s_cg[NW];
   __shared__ double s_b[L];
-  uint16_t* s_K = reinterpret_cast<uint16_t*>(smem);
-  uint16_t* s_Q = s_K + NP * W::kPlane;
-  uint16_t* s_dP = s_Q + NP * W::kPlane;
+  uint16_t* s_K = reinterpret_cast<uint16_t*>(smem);  // and Q
+  uint16_t* s_dP = s_K + NP * W::kPlane;
   uint16_t* s_dA = s_dP + 3 * W::kPlaneS;
 
   const int bh = blockIdx.x / p.Nc, c = blockIdx.x % p.Nc, t0 = c * L;
@@ -119,21 +123,22 @@ delta_grads_kernel(const DeltaParams p) {
   const int DV = p.DV;
   if (tid < L) s_b[tid] = p.bsum[at * L + tid];
 
-  float4_t dq[2][RT], dk[2][RT], hu[TPW], ru[TPW];
+  float4_t dq[KPW][RT], dk[KPW][RT], hu[TPW], ru[TPW];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < KPW; ++i)
 #pragma unroll
     for (int j = 0; j < RT; ++j) dq[i][j] = dk[i][j] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < TPW; ++i) hu[i] = ru[i] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
   float cg = 0.0f, dvu[ROWS], vdv[ROWS], qe[ROWS], qw[ROWS];
 
-  // this wave's 32 rows of the states, this thread's quads of the rest
-  const uint32_t rows_bytes = 32u * (uint32_t)DV * 4u;
-  const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.C_states + (at * DK + 32 * __builtin_amdgcn_readfirstlane(wave)) * DV, rows_bytes);
-  const __amdgpu_buffer_rsrc_t rg = make_rsrc(p.G_states + (at * DK + 32 * __builtin_amdgcn_readfirstlane(wave)) * DV, rows_bytes);
+  // this wave's rows of the states, this thread's quads of the rest
+  const uint32_t rows_bytes = 16u * KPW * (uint32_t)DV * 4u;
+  const size_t first = (at * DK + 16 * KPW * __builtin_amdgcn_readfirstlane(wave)) * DV;
+  const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.C_states + first, rows_bytes);
+  const __amdgpu_buffer_rsrc_t rg = make_rsrc(p.G_states + first, rows_bytes);
   const int state_off = 4 * (row * DV + 8 * grp), row16 = 64 * DV;
-  StateRows xc, xg, nc, ng;
+  StateRows<KPW> xc, xg;
   Quad<float> qu[ROWS], qr[ROWS];
   Quad<TH> qh[ROWS];
   Quad<TIn> qv[ROWS];
@@ -184,19 +189,13 @@ delta_grads_kernel(const DeltaParams p) {
   if (DV > 32) fetch(32);
 
   for (int v0 = 0; v0 < DV; v0 += 32) {
-    const uint16_t* s = s_K + ((v0 >> 5) & 1) * W::kStage;
-    __syncthreads();  // this step is staged, the one before read out
-    if (v0 + 32 < DV) {
-      nc.load(rc, state_off, row16, v0 + 32);
-      ng.load(rg, state_off, row16, v0 + 32);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-
+    const uint16_t* s = s_K + (W::BUFS == 2 ? ((v0 >> 5) & 1) * W::kStage : 0);
+    __syncthreads();  // this step is staged (and with two buffers the one before read out)
     // the products with the states: rows of C and G, columns t
-    Parts<3> cp[2];
-    Parts<NB> gp[2];
+    Parts<3> cp[KPW];
+    Parts<NB> gp[KPW];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < KPW; ++i) {
       float a[8], b[8];
       xc.values(i, a);
       xg.values(i, b);
@@ -205,13 +204,18 @@ delta_grads_kernel(const DeltaParams p) {
       cp[i] = split_parts<3>(a);
       gp[i] = split_parts<NB>(b);
     }
+    if (v0 + 32 < DV) {
+      xc.load(rc, state_off, row16, v0 + 32);
+      xg.load(rg, state_off, row16, v0 + 32);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
       const uint16_t* o = s + (16 * j + row) * W::kLdT + 8 * grp;
       const Parts<NH> h = lds_row8<NH>(o, W::kPlaneT);
       const Parts<NB> r = lds_row8<NB>(o + W::kRe, W::kPlaneT), u = lds_row8<NB>(o + W::kUw, W::kPlaneT);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < KPW; ++i) {
         dq[i][j] = mma_parts<3, NH>(cp[i], h, dq[i][j]);
         dk[i][j] = mma_parts<NB, NB>(first_parts<NB>(cp[i]), r, dk[i][j]);
         dk[i][j] = mma_parts<NB, NB>(gp[i], u, dk[i][j]);
@@ -231,13 +235,12 @@ delta_grads_kernel(const DeltaParams p) {
     }
     __builtin_amdgcn_sched_barrier(0);
     if (v0 + 32 < DV) {
-      stage(s_K + (((v0 >> 5) + 1) & 1) * W::kStage);
+      if (W::BUFS == 1) __syncthreads();  // read out
+      stage(s_K + (W::BUFS == 2 ? (((v0 >> 5) + 1) & 1) * W::kStage : 0));
       if (v0 + 64 < DV) fetch(v0 + 64);
     }
-    xc = nc;
-    xg = ng;
   }
-  __syncthreads();  // the staged columns are read out: K and Q take their place
+  __syncthreads();  // the staged columns are read out: K takes their place
 
   // row sums of the staged quads, eight lanes a row
 #pragma unroll
@@ -263,11 +266,10 @@ delta_grads_kernel(const DeltaParams p) {
   const TIn* K = static_cast<const TIn*>(p.K) + (size_t)bh * p.S * DK;
   const TIn* Q = static_cast<const TIn*>(p.Q) + (size_t)bh * p.S * DK;
   stage_rows<TIn, L, DK>(s_K, W::kLd, W::kPlane, K, t0, p.S, tid, THREADS);
-  stage_rows<TIn, L, DK>(s_Q, W::kLd, W::kPlane, Q, t0, p.S, tid, THREADS);
   __syncthreads();
-  auto put = [&](uint16_t* dst, float x) {
+  auto put = [&](uint16_t* dst, float x, int parts) {
 #pragma unroll
-    for (int n = 0; n < 3; ++n) {
+    for (int n = 0; n < parts; ++n) {
       const uint32_t u = __float_as_uint(x);
       dst[n * W::kPlaneS] = (uint16_t)(u >> 16);
       x -= __uint_as_float(u & 0xffff0000u);
@@ -284,10 +286,10 @@ delta_grads_kernel(const DeltaParams p) {
       const int t = 16 * rt + 4 * grp + r, j = 16 * ct + row;
       if (j <= t) {
         const float D = expf((float)(s_b[t] - s_b[j]));
-        put(s_dP + t * W::kLdS + j, p.scale * D * hu[i][r]);
+        put(s_dP + t * W::kLdS + j, p.scale * D * hu[i][r], 3);
         const float a = j < t ? -D * ru[i][r] : 0.0f;
-        put(s_dA + t * W::kLdS + j, a);
-        if (j < t) put(s_dA + j * W::kLdS + t, a);
+        put(s_dA + t * W::kLdS + j, a, NB);
+        if (j < t) put(s_dA + j * W::kLdS + t, a, NB);
       }
     }
   }
@@ -299,26 +301,34 @@ delta_grads_kernel(const DeltaParams p) {
     const int t = 16 * j + row;
     const float se = p.scale * p.e[at * L + t];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) dq[i][j] *= se;
+    for (int i = 0; i < KPW; ++i) dq[i][j] *= se;
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int k0 = 32 * wave + 16 * i;
+  for (int i = 0; i < KPW; ++i)
 #pragma unroll
     for (int s = 0; s < L / 32; ++s) {
-      const Parts<NP> kt = lds_col<NP>(s_K, W::kLd, W::kPlane, 32 * s + 8 * grp, 4, k0, lane);
-      const Parts<NP> qt = lds_col<NP>(s_Q, W::kLd, W::kPlane, 32 * s + 8 * grp, 4, k0, lane);
+      const Parts<NP> kt = lds_col<NP>(s_K, W::kLd, W::kPlane, 32 * s + 8 * grp, 4, 16 * (KPW * wave + i), lane);
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
         const int o = (16 * j + row) * W::kLdS + 32 * s + 8 * grp;
         if (s <= j / 2) dq[i][j] = mma_parts<NP, 3>(kt, lds_row8<3>(s_dP + o, W::kPlaneS), dq[i][j]);
-        if (s >= j / 2)
-          dk[i][j] = mma_parts<NP, NB>(qt, lds_col<NB>(s_dP, W::kLdS, W::kPlaneS, 32 * s + 8 * grp, 4, 16 * j, lane),
-                                        dk[i][j]);
         dk[i][j] = mma_parts<NP, NB>(kt, lds_row8<NB>(s_dA + o, W::kPlaneS), dk[i][j]);
       }
     }
-  }
+  __syncthreads();
+  stage_rows<TIn, L, DK>(s_K, W::kLd, W::kPlane, Q, t0, p.S, tid, THREADS);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < KPW; ++i)
+#pragma unroll
+    for (int s = 0; s < L / 32; ++s) {
+      const Parts<NP> qt = lds_col<NP>(s_K, W::kLd, W::kPlane, 32 * s + 8 * grp, 4, 16 * (KPW * wave + i), lane);
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+        if (s >= j / 2)
+          dk[i][j] = mma_parts<NP, NB>(qt, lds_col<NB>(s_dP, W::kLdS, W::kPlaneS, 32 * s + 8 * grp, 4, 16 * j, lane),
+                                       dk[i][j]);
+    }
 
   // store, and q . dq by rows
 #pragma unroll
@@ -326,13 +336,13 @@ delta_grads_kernel(const DeltaParams p) {
     const int t = 16 * j + row;
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k0 = 32 * wave + 16 * i + 4 * grp;
+    for (int i = 0; i < KPW; ++i) {
+      const int k0 = 16 * (KPW * wave + i) + 4 * grp;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float q = 0.0f;
 #pragma unroll
-        for (int n = NP - 1; n >= 0; --n) q += bf16_to_f32(s_Q[n * W::kPlane + t * W::kLd + k0 + r]);
+        for (int n = NP - 1; n >= 0; --n) q += bf16_to_f32(s_K[n * W::kPlane + t * W::kLd + k0 + r]);
         dot += q * dq[i][j][r];
       }
       if (t0 + t < p.S) {
@@ -382,11 +392,11 @@ delta_grads_kernel(const DeltaParams p) {
 
 template <typename TIn, typename TH>
 hipError_t launch_types(const DeltaParams& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((long long)p.BH * p.Nc)), block(2 * p.DK);
+  const dim3 grid((unsigned)((long long)p.BH * p.Nc));
   switch (p.DK) {
-    case 64: hipLaunchKernelGGL((delta_grads_kernel<TIn, TH, 64>), grid, block, 0, stream, p); break;
-    case 128: hipLaunchKernelGGL((delta_grads_kernel<TIn, TH, 128>), grid, block, 0, stream, p); break;
-    case 256: hipLaunchKernelGGL((delta_grads_kernel<TIn, TH, 256>), grid, block, 0, stream, p); break;
+    case 64: hipLaunchKernelGGL((delta_grads_kernel<TIn, TH, 64>), grid, dim3(64 * GradLds<TIn, TH, 64>::NW), 0, stream, p); break;
+    case 128: hipLaunchKernelGGL((delta_grads_kernel<TIn, TH, 128>), grid, dim3(64 * GradLds<TIn, TH, 128>::NW), 0, stream, p); break;
+    case 256: hipLaunchKernelGGL((delta_grads_kernel<TIn, TH, 256>), grid, dim3(64 * GradLds<TIn, TH, 256>::NW), 0, stream, p); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
