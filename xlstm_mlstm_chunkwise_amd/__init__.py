@@ -12,6 +12,7 @@ import of the functions below fails with an error that says how to build it.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -736,10 +737,13 @@ def _out_code(dtype, name) -> int:
     raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
 
 
-def _check_same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _check_on(dev, name, t, shape, dtype):
+    """_check for a tensor that has to be on dev (None passes)."""
+    if t is None:
+        return
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        _check(t, name, shape, dtype)
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
 def _call(where, dev, *args):
@@ -748,10 +752,10 @@ def _call(where, dev, *args):
     torch = _torch()
     fn = getattr(lib(), where)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if st:
         raise MlstmError(st, where)
 
@@ -759,22 +763,45 @@ def _call(where, dev, *args):
 def _bytes_of(need, workspace, dev):
     torch = _torch()
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
+    if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
+    if workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
     size = workspace.numel() * workspace.element_size()
     if size < need:
         raise ValueError(f"workspace holds {size} bytes, need {need}")
     return workspace, size
 
 
-def _delta_desc(where, q, v, lead, S, h_dtype, qk_scale):
-    desc = make_delta_desc(*lead, S, q.shape[-1], v.shape[-1], qkv_dtype=_dtype_code(q),
+@functools.lru_cache(maxsize=256)
+def _delta_plan(where, B, NH, S, DK, DV, qkv_dtype, h_dtype, qk_scale):
+    """Descriptor (as an argument) and workspace sizes, forward and backward."""
+    desc = make_delta_desc(B, NH, S, DK, DV, qkv_dtype=_out_code(qkv_dtype, "Q/K/V"),
                            h_dtype=_out_code(h_dtype, "h_dtype"), qk_scale=0.0 if qk_scale is None else float(qk_scale))
     st = delta_validate(desc)
     if st:
         raise MlstmError(st, where)
-    return desc
+    return ctypes.byref(desc), delta_fw_workspace_bytes(desc), delta_bw_workspace_bytes(desc)
+
+
+def _delta_inputs(q, k, v, i_pre, f_pre, C0):
+    """Shapes of the sequence's inputs, checked."""
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError("Q must be (B, NH, S, DHQK)")
+    B, NH, S, DK = q.shape
+    DV = v.shape[-1]
+    dev = q.device
+    if not q.is_cuda:
+        raise ValueError("Q must be a GPU tensor")
+    _check_on(dev, "Q", q, (B, NH, S, DK), q.dtype)
+    _check_on(dev, "K", k, (B, NH, S, DK), q.dtype)
+    _check_on(dev, "V", v, (B, NH, S, DV), q.dtype)
+    _check_on(dev, "i_pre", i_pre, (B, NH, S), torch.float32)
+    _check_on(dev, "f_pre", f_pre, (B, NH, S), torch.float32)
+    _check_on(dev, "C0", C0, (B, NH, DK, DV), torch.float32)
+    return B, NH, S, DK, DV
 
 
 def mlstm_delta_fw(q, k, v, i_pre, f_pre, C0=None, *, h_dtype=None, qk_scale: Optional[float] = None,
@@ -789,17 +816,15 @@ def mlstm_delta_fw(q, k, v, i_pre, f_pre, C0=None, *, h_dtype=None, qk_scale: Op
     sigmoid(i_pre) |k|^2 < 2 the state stays bounded.
     """
     torch = _torch()
-    B, NH, S, DK, DV = _check_inputs(q, k, v, i_pre, f_pre)
-    h_dtype = h_dtype or (torch.float32 if out is None else out.dtype)
-    _check(C0, "C0", (B, NH, DK, DV), torch.float32)
-    _check(out, "H", (B, NH, S, DV), h_dtype)
+    B, NH, S, DK, DV = _delta_inputs(q, k, v, i_pre, f_pre, C0)
     dev = q.device
-    _check_same_device(dev, K=k, V=v, i_pre=i_pre, f_pre=f_pre, C0=C0, H=out, workspace=workspace)
-    desc = _delta_desc("mlstm_delta_fw", q, v, (B, NH), S, h_dtype, qk_scale)
-    workspace, ws_bytes = _bytes_of(delta_fw_workspace_bytes(desc), workspace, dev)
+    h_dtype = h_dtype or (torch.float32 if out is None else out.dtype)
+    _check_on(dev, "H", out, (B, NH, S, DV), h_dtype)
+    desc, need, _ = _delta_plan("mlstm_delta_fw", B, NH, S, DK, DV, q.dtype, h_dtype, qk_scale)
+    workspace, ws_bytes = _bytes_of(need, workspace, dev)
     H = torch.empty((B, NH, S, DV), dtype=h_dtype, device=dev) if out is None else out
     C = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev) if return_final_state else None
-    _call("mlstm_delta_fw", dev, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C0),
+    _call("mlstm_delta_fw", dev, desc, _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C0),
           _ptr(H), _ptr(C), _ptr(workspace), ws_bytes)
     return H, C
 
@@ -813,19 +838,17 @@ def mlstm_delta_bw(q, k, v, i_pre, f_pre, dH, C0=None, dC=None, *, qk_scale: Opt
     dict with dQ, dK, dV (q's dtype), d_i, d_f (float32) and, with
     state_grads, dC0 (float32)."""
     torch = _torch()
-    B, NH, S, DK, DV = _check_inputs(q, k, v, i_pre, f_pre)
-    _check(dH, "dH", (B, NH, S, DV))
-    _check(C0, "C0", (B, NH, DK, DV), torch.float32)
-    _check(dC, "dC", (B, NH, DK, DV), torch.float32)
+    B, NH, S, DK, DV = _delta_inputs(q, k, v, i_pre, f_pre, C0)
     dev = q.device
-    _check_same_device(dev, K=k, V=v, i_pre=i_pre, f_pre=f_pre, dH=dH, C0=C0, dC=dC, workspace=workspace)
-    desc = _delta_desc("mlstm_delta_bw", q, v, (B, NH), S, dH.dtype, qk_scale)
-    workspace, ws_bytes = _bytes_of(delta_bw_workspace_bytes(desc), workspace, dev)
+    _check_on(dev, "dH", dH, (B, NH, S, DV), dH.dtype)
+    _check_on(dev, "dC", dC, (B, NH, DK, DV), torch.float32)
+    desc, _, need = _delta_plan("mlstm_delta_bw", B, NH, S, DK, DV, q.dtype, dH.dtype, qk_scale)
+    workspace, ws_bytes = _bytes_of(need, workspace, dev)
     g = dict(dQ=torch.empty_like(q), dK=torch.empty_like(k), dV=torch.empty_like(v), d_i=torch.empty_like(i_pre),
              d_f=torch.empty_like(f_pre))
     if state_grads:
         g["dC0"] = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev)
-    _call("mlstm_delta_bw", dev, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C0),
+    _call("mlstm_delta_bw", dev, desc, _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C0),
           _ptr(dH), _ptr(dC), _ptr(g["dQ"]), _ptr(g["dK"]), _ptr(g["dV"]), _ptr(g["d_i"]), _ptr(g["d_f"]),
           _ptr(g.get("dC0")), _ptr(workspace), ws_bytes)
     return g
@@ -840,23 +863,24 @@ def mlstm_delta_step(q, k, v, i_pre, f_pre, C=None, *, h_dtype=None, qk_scale: O
     torch = _torch()
     if q.dim() != 3:
         raise ValueError("q must be (B, NH, DHQK)")
+    if not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
     B, NH, DK = q.shape
     DV = v.shape[-1]
-    _check(q, "q", (B, NH, DK))
-    _check(k, "k", (B, NH, DK), q.dtype)
-    _check(v, "v", (B, NH, DV), q.dtype)
-    _check(i_pre, "i_pre", (B, NH), torch.float32)
-    _check(f_pre, "f_pre", (B, NH), torch.float32)
-    _check(C, "C", (B, NH, DK, DV), torch.float32)
-    _check(C_out, "C_out", (B, NH, DK, DV), torch.float32)
     dev = q.device
-    _check_same_device(dev, k=k, v=v, i_pre=i_pre, f_pre=f_pre, C=C, C_out=C_out)
+    _check_on(dev, "q", q, (B, NH, DK), q.dtype)
+    _check_on(dev, "k", k, (B, NH, DK), q.dtype)
+    _check_on(dev, "v", v, (B, NH, DV), q.dtype)
+    _check_on(dev, "i_pre", i_pre, (B, NH), torch.float32)
+    _check_on(dev, "f_pre", f_pre, (B, NH), torch.float32)
+    _check_on(dev, "C", C, (B, NH, DK, DV), torch.float32)
+    _check_on(dev, "C_out", C_out, (B, NH, DK, DV), torch.float32)
     h_dtype = h_dtype or torch.float32
-    desc = _delta_desc("mlstm_delta_step", q, v, (B, NH), 1, h_dtype, qk_scale)
+    desc, _, _ = _delta_plan("mlstm_delta_step", B, NH, 1, DK, DV, q.dtype, h_dtype, qk_scale)
     h = torch.empty((B, NH, DV), dtype=h_dtype, device=dev)
     if C_out is None:
         C_out = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev)
-    _call("mlstm_delta_step", dev, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C),
+    _call("mlstm_delta_step", dev, desc, _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C),
           _ptr(h), _ptr(C_out))
     return h, C_out
 
@@ -924,15 +948,25 @@ def head_norm_bw_workspace_bytes(desc: HeadNormDesc) -> int:
     return lib().mlstm_head_norm_bw_workspace_bytes(ctypes.byref(desc))
 
 
-def _norm_desc(where, x, y_dtype, eps):
-    if x.dim() != 4:
-        raise ValueError("x must be (B, NH, S, D)")
-    desc = make_head_norm_desc(*x.shape, x_dtype=_out_code(x.dtype, "x"), y_dtype=_out_code(y_dtype, "y_dtype"),
+@functools.lru_cache(maxsize=256)
+def _norm_plan(where, B, NH, S, D, x_dtype, y_dtype, eps):
+    """Descriptor (as an argument) and the backward pass's workspace size."""
+    desc = make_head_norm_desc(B, NH, S, D, x_dtype=_out_code(x_dtype, "x"), y_dtype=_out_code(y_dtype, "y_dtype"),
                                eps=float(eps))
     st = head_norm_validate(desc)
     if st:
         raise MlstmError(st, where)
-    return desc
+    return ctypes.byref(desc), head_norm_bw_workspace_bytes(desc)
+
+
+def _norm_input(x):
+    if x.dim() != 4:
+        raise ValueError("x must be (B, NH, S, D)")
+    _out_code(x.dtype, "x")
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    _check_on(x.device, "x", x, x.shape, x.dtype)
+    return x.shape
 
 
 def head_norm_fw(x, weight=None, bias=None, *, eps: float = 1e-6, y_dtype=None, out=None):
@@ -942,17 +976,15 @@ def head_norm_fw(x, weight=None, bias=None, *, eps: float = 1e-6, y_dtype=None, 
     projection, in y_dtype (x's dtype unless given); D is a multiple of 64 up
     to 512, x and y bfloat16 or float32."""
     torch = _torch()
-    y_dtype = y_dtype or (x.dtype if out is None else out.dtype)
-    desc = _norm_desc("mlstm_head_norm_fw", x, y_dtype, eps)
-    B, NH, S, D = x.shape
-    _check(x, "x", (B, NH, S, D))
-    _check(weight, "weight", (NH, D), torch.float32)
-    _check(bias, "bias", (NH, D), torch.float32)
-    _check(out, "y", (B, S, NH, D), y_dtype)
+    B, NH, S, D = _norm_input(x)
     dev = x.device
-    _check_same_device(dev, weight=weight, bias=bias, y=out)
+    y_dtype = y_dtype or (x.dtype if out is None else out.dtype)
+    _check_on(dev, "weight", weight, (NH, D), torch.float32)
+    _check_on(dev, "bias", bias, (NH, D), torch.float32)
+    _check_on(dev, "y", out, (B, S, NH, D), y_dtype)
+    desc, _ = _norm_plan("mlstm_head_norm_fw", B, NH, S, D, x.dtype, y_dtype, eps)
     y = torch.empty((B, S, NH, D), dtype=y_dtype, device=dev) if out is None else out
-    _call("mlstm_head_norm_fw", dev, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y))
+    _call("mlstm_head_norm_fw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y))
     return y
 
 
@@ -961,18 +993,16 @@ def head_norm_bw(x, dy, weight=None, *, eps: float = 1e-6, weight_grads: bool = 
     dweight, dbias) from x, dy (B, S, NH, D) and the weight; dx in x's dtype,
     dweight and dbias (NH, D) float32, None without weight_grads."""
     torch = _torch()
-    desc = _norm_desc("mlstm_head_norm_bw", x, dy.dtype, eps)
-    B, NH, S, D = x.shape
-    _check(x, "x", (B, NH, S, D))
-    _check(dy, "dy", (B, S, NH, D))
-    _check(weight, "weight", (NH, D), torch.float32)
+    B, NH, S, D = _norm_input(x)
     dev = x.device
-    _check_same_device(dev, dy=dy, weight=weight, workspace=workspace)
+    _check_on(dev, "dy", dy, (B, S, NH, D), dy.dtype)
+    _check_on(dev, "weight", weight, (NH, D), torch.float32)
+    desc, need = _norm_plan("mlstm_head_norm_bw", B, NH, S, D, x.dtype, dy.dtype, eps)
     dx, dw, db, ws_bytes = torch.empty_like(x), None, None, 0
     if weight_grads:
-        workspace, ws_bytes = _bytes_of(head_norm_bw_workspace_bytes(desc), workspace, dev)
+        workspace, ws_bytes = _bytes_of(need, workspace, dev)
         dw, db = (torch.empty((NH, D), dtype=torch.float32, device=dev) for _ in range(2))
-    _call("mlstm_head_norm_bw", dev, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
+    _call("mlstm_head_norm_bw", dev, desc, _ptr(x), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
           _ptr(workspace), ws_bytes)
     return dx, dw, db
 

@@ -358,6 +358,41 @@ struct TileStage {
   }
 };
 
+// The same for W of the DK columns, in a tile of that width.
+template <typename TIn, int DK, int W, int THREADS>
+struct PartStage {
+  static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts;
+  static constexpr int kRow = W / 8, kN = L * kRow / THREADS, kWords = sizeof(TIn) == 2 ? 1 : 2;
+  words4_t x[kN * kWords];
+
+  static_assert(kN * THREADS == L * kRow, "whole rounds");
+  // src: the chunk's first row at the first column, which is column `col`
+  __device__ __forceinline__ void load(const TIn* src, int col, int rows, int tid) {
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(src, (uint32_t)__builtin_amdgcn_readfirstlane((rows * DK - col) * (int)sizeof(TIn)));
+    int off = (tid / kRow * DK + 8 * (tid % kRow)) * (int)sizeof(TIn);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+        x[n * kWords + w] = __builtin_bit_cast(words4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16 * w, 0, 0));
+      off += THREADS / kRow * DK * (int)sizeof(TIn);
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* dst, int plane, int tid) const {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      uint16_t* o = dst + tile_at<W>(tid / kRow + n * (THREADS / kRow), tid % kRow);
+      if constexpr (sizeof(TIn) == 2) {
+        *reinterpret_cast<words4_t*>(o) = x[n];
+      } else {
+        const float4 a = __builtin_bit_cast(float4, x[n * kWords]), b = __builtin_bit_cast(float4, x[n * kWords + kWords - 1]);
+        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        store_parts<NP>(o, plane, split_parts<NP>(v));
+      }
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------
 // T and P of a chunk in operand order.  A lower triangular L x L matrix M is
 // the left operand of a product over its columns as fragments (row tile rt,

@@ -32,12 +32,13 @@ template <typename TIn, int DK, bool BACK>
 __global__ __launch_bounds__(4 * DeltaIn<TIn>::kChunk) void delta_prep_kernel(const DeltaParams p) {
   constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts, RT = L / 16, THREADS = 4 * L;
   constexpr int LDA = L + 4;
-  constexpr int kTiles = 2 * NP * L * DK * 2, kSquares = 2 * L * LDA * 4;
+  constexpr int W = DK < 128 ? DK : 128;  // columns of K and Q at a time: four workgroups fit a CU
+  constexpr int kTiles = 2 * NP * L * W * 2, kSquares = 2 * L * LDA * 4;
   __shared__ double s_b[L];
   __shared__ float s_beta[L];
   __shared__ uint4 smem[(kTiles > kSquares ? kTiles : kSquares) / 16];
   uint16_t* s_K = reinterpret_cast<uint16_t*>(smem);  // first K and Q,
-  uint16_t* s_Q = s_K + NP * L * DK;
+  uint16_t* s_Q = s_K + NP * L * W;
   float* s_A = reinterpret_cast<float*>(smem);        // then the squares
   float* s_T = s_A + L * LDA;
 
@@ -47,10 +48,12 @@ __global__ __launch_bounds__(4 * DeltaIn<TIn>::kChunk) void delta_prep_kernel(co
   const int row = lane & 15, grp = lane >> 4;
   const size_t at = (size_t)bh * p.Nc + c;
 
-  TileStage<TIn, DK, THREADS> gk, gq;
+  PartStage<TIn, DK, W, THREADS> gk, gq;
   const int rows = p.S - t0 < L ? p.S - t0 : L;
-  gk.load(static_cast<const TIn*>(p.K) + ((size_t)bh * p.S + t0) * DK, rows, tid);
-  gq.load(static_cast<const TIn*>(p.Q) + ((size_t)bh * p.S + t0) * DK, rows, tid);
+  const TIn* K = static_cast<const TIn*>(p.K) + ((size_t)bh * p.S + t0) * DK;
+  const TIn* Q = static_cast<const TIn*>(p.Q) + ((size_t)bh * p.S + t0) * DK;
+  gk.load(K, 0, rows, tid);
+  gq.load(Q, 0, rows, tid);
   if (wave == 0) {
     const int t = t0 + lane;
     const bool in = lane < L && t < p.S;
@@ -75,20 +78,28 @@ __global__ __launch_bounds__(4 * DeltaIn<TIn>::kChunk) void delta_prep_kernel(co
   float4_t kk[RT], qk[RT];
 #pragma unroll
   for (int j = 0; j < RT; ++j) kk[j] = qk[j] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-  gk.store(s_K, L * DK, tid);
-  gq.store(s_Q, L * DK, tid);
-  __syncthreads();
-  const int seed = tile_row_seed<DK>(row, grp);
+  const int seed = tile_row_seed<W>(row, grp);
 #pragma unroll
-  for (int ks = 0; ks < DK / 32; ++ks) {
-    const Parts<NP> ka = tile_row<NP, DK>(s_K, L * DK, seed, wave, ks);
-    const Parts<NP> qa = tile_row<NP, DK>(s_Q, L * DK, seed, wave, ks);
+  for (int c0 = 0; c0 < DK; c0 += W) {
+    if (c0) __syncthreads();
+    gk.store(s_K, L * W, tid);
+    gq.store(s_Q, L * W, tid);
+    __syncthreads();
+    if (c0 + W < DK) {
+      gk.load(K + c0 + W, c0 + W, rows, tid);
+      gq.load(Q + c0 + W, c0 + W, rows, tid);
+    }
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      if (j > wave) continue;
-      const Parts<NP> kb = tile_row<NP, DK>(s_K, L * DK, seed, j, ks);
-      kk[j] = mma_parts<NP, NP>(ka, kb, kk[j]);
-      qk[j] = mma_parts<NP, NP>(qa, kb, qk[j]);
+    for (int ks = 0; ks < W / 32; ++ks) {
+      const Parts<NP> ka = tile_row<NP, W>(s_K, L * W, seed, wave, ks);
+      const Parts<NP> qa = tile_row<NP, W>(s_Q, L * W, seed, wave, ks);
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        if (j > wave) continue;
+        const Parts<NP> kb = tile_row<NP, W>(s_K, L * W, seed, j, ks);
+        kk[j] = mma_parts<NP, NP>(ka, kb, kk[j]);
+        qk[j] = mma_parts<NP, NP>(qa, kb, qk[j]);
+      }
     }
   }
   __syncthreads();

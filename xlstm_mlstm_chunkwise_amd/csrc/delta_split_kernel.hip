@@ -21,41 +21,6 @@
 namespace mlstm {
 namespace {
 
-// Rows [0, L) and this wave's W columns of a K or Q tile on their way from
-// memory to the wave's own LDS.
-template <typename TIn, int DK, int W>
-struct PartStage {
-  static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts;
-  static constexpr int kRow = W / 8, kN = L * kRow / 64, kWords = sizeof(TIn) == 2 ? 1 : 2;
-  words4_t x[kN * kWords];
-
-  // src: the chunk's first row at the wave's first column, `col` columns into the row
-  __device__ __forceinline__ void load(const TIn* src, int col, int rows, int lane) {
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(src, (uint32_t)__builtin_amdgcn_readfirstlane((rows * DK - col) * (int)sizeof(TIn)));
-    int off = (lane / kRow * DK + 8 * (lane % kRow)) * (int)sizeof(TIn);
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-#pragma unroll
-      for (int w = 0; w < kWords; ++w)
-        x[n * kWords + w] = __builtin_bit_cast(words4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16 * w, 0, 0));
-      off += 64 / kRow * DK * (int)sizeof(TIn);
-    }
-  }
-  __device__ __forceinline__ void store(uint16_t* dst, int plane, int lane) const {
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      uint16_t* o = dst + tile_at<W>(lane / kRow + n * (64 / kRow), lane % kRow);
-      if constexpr (sizeof(TIn) == 2) {
-        *reinterpret_cast<words4_t*>(o) = x[n];
-      } else {
-        const float4 a = __builtin_bit_cast(float4, x[n * kWords]), b = __builtin_bit_cast(float4, x[n * kWords + kWords - 1]);
-        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        store_parts<NP>(o, plane, split_parts<NP>(v));
-      }
-    }
-  }
-};
-
 template <typename TIn, int DK>
 struct SplitShape {
   static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts;
@@ -238,7 +203,7 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ke
   for (int k = 0; k < KT; ++k) C[k] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
   if (p.C0) load_whole(Slice<float>(p.C0 + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), C);
 
-  PartStage<TIn, DK, W> gk, gq;
+  PartStage<TIn, DK, W, 64> gk, gq;
   Parts<3> gt[OWN][TS];
   Parts<PP> gp[OWN][TS];
   OneTile<TIn> gv[OWN];
@@ -398,7 +363,7 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ba
   for (int k = 0; k < KT; ++k) G[k] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
   if (p.dC_out) load_whole(Slice<float>(p.dC_out + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), G);
 
-  PartStage<TIn, DK, W> gk, gq;
+  PartStage<TIn, DK, W, 64> gk, gq;
   Parts<3> gt[OWN][TS], gp[OWN][TS];
   OneTile<TH> gh[OWN];
   OneTile<float> gu[OWN];
