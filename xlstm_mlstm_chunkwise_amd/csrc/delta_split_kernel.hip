@@ -4,9 +4,10 @@
 // The walk of delta_walk_kernel.hip gives a wave sixteen value columns of one
 // head; with few heads that leaves most of the chip idle and a chunk takes as
 // long as one wave's products.  Here the waves of a workgroup share sixteen
-// columns: wave i holds rows i DHQK / RW .. of the state.  Per chunk
+// columns: wave i holds rows i DHQK / RW .. of the state (two waves at DHQK 64,
+// four above) and owns row tile i of the chunk's sixteen-token tiles.  Per chunk
 //   - each wave forms its rows' share of K C and Q C (L x 16); the shares meet
-//     in LDS, where each row tile of sixteen tokens has one owning wave;
+//     in LDS;
 //   - the owner forms its tile of V - e K C, which all owners read as operand,
 //     its tile of U = T (..), which all waves read, and its tile of H;
 //   - each wave updates its own rows, C <- g C + K^T (w U).
@@ -24,20 +25,14 @@ namespace {
 template <typename TIn, int DK>
 struct SplitShape {
   static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts;
-  static constexpr int RW = DK == 64 ? 2 : 4;           // waves
-  static constexpr int W = DK / RW;                     // state rows a wave
   static constexpr int RT = L / 16, TS = L / 32;
-  static constexpr int OWN = RT > RW ? RT / RW : 1;     // row tiles an owner
+  static constexpr int RW = DK == 64 ? 2 : 4;           // waves that hold rows of the state
+  static constexpr int W = DK / RW;                     // rows each
+  static constexpr int NW = RT > RW ? RT : RW;          // waves: wave i owns row tile i
+  static constexpr int kSlots = RT > RW ? RW : RW - 1;  // shares an owner receives, at most
   static constexpr int kPlane = L * W, kTile = NP * kPlane;
   static constexpr int kFragWords = kFragElems / 2;     // one operand fragment plane, in 32-bit words
 };
-
-// The i-th row tile of a wave (a tile past the last: the wave owns none).
-// Two tiles a wave go in pairs of equal work under the triangle.
-template <typename S>
-__device__ __forceinline__ int own_tile(int wave, int i) {
-  return S::OWN == 1 ? wave : (i == 0 ? wave : S::RT - 1 - wave);
-}
 
 // One owner's tile of an operand (four values a lane) into the fragment of
 // its 32-row block, N parts.
@@ -80,18 +75,19 @@ __device__ __forceinline__ void tile_times(const Parts<NM> (&m)[L / 32], const u
     for (int ts = 0; ts < TS; ++ts) acc += sum[ts][k];
 }
 
-// The fragments of row tile rt, from memory (zeros where the triangle has none).
+// The fragments of row tile rt, from memory (zeros where the triangle has none:
+// the resource is empty).
 template <int L, bool UP, int NM>
 __device__ __forceinline__ void load_square_rows(const uint16_t* M, int rt, Parts<NM> (&m)[L / 32], int lane) {
-  const __amdgpu_buffer_rsrc_t r = make_rsrc(M, square_frags<L>() * NM * kFragElems * 2);
 #pragma unroll
   for (int ts = 0; ts < L / 32; ++ts) {
     const bool in = rt < L / 16 && (UP ? ts >= (rt >> 1) : ts <= (rt >> 1));
     const int f = L != 64 ? rt : UP ? (rt < 2 ? 2 * rt + ts : rt + 2) : (rt < 2 ? rt : 2 * rt - 2 + ts);
+    const __amdgpu_buffer_rsrc_t r =
+        make_rsrc(M + (in ? f * NM * kFragElems : 0), (uint32_t)__builtin_amdgcn_readfirstlane(in ? NM * kFragElems * 2 : 0));
 #pragma unroll
     for (int n = 0; n < NM; ++n)
-      m[ts].p[n] = __builtin_bit_cast(
-          bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(r, in ? (f * NM + n) * 2 * kFragElems + 16 * lane : 1 << 30, 0, 0));
+      m[ts].p[n] = __builtin_bit_cast(bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(r, 16 * lane + 2 * n * kFragElems, 0, 0));
   }
 }
 
@@ -119,14 +115,12 @@ __device__ __forceinline__ void state_parts(const float4_t (&C)[W / 16], Parts<3
 }
 
 // The shares of the waves, one 1 KiB slot per row tile and sending wave; an
-// owner adds its own from registers.
+// owner with rows of its own adds that share from registers.
 template <typename S>
 __device__ __forceinline__ void send_shares(float4_t* slots, const float4_t (&x)[S::RT], int wave, int lane) {
 #pragma unroll
-  for (int rt = 0; rt < S::RT; ++rt) {
-    const int owner = S::OWN == 1 ? rt : (rt < S::RW ? rt : S::RT - 1 - rt);
-    if (owner != wave) slots[(rt * (S::RW - 1) + (wave < owner ? wave : wave - 1)) * 64 + lane] = x[rt];
-  }
+  for (int rt = 0; rt < S::RT; ++rt)
+    if (rt != wave) slots[(rt * S::kSlots + (rt >= S::RW || wave < rt ? wave : wave - 1)) * 64 + lane] = x[rt];
 }
 template <typename S>
 __device__ __forceinline__ float4_t take_shares(const float4_t* slots, const float4_t (&x)[S::RT], int rt, int lane) {
@@ -135,24 +129,27 @@ __device__ __forceinline__ float4_t take_shares(const float4_t* slots, const flo
   for (int i = 0; i < S::RT; ++i) {
     float4_t own = x[i];
     asm("" : "+v"(own));  // a value each: as an indexed array the tiles would leave the registers
-    if (rt == i) v = own;
+    if (rt == i && rt < S::RW) v = own;
   }
 #pragma unroll
-  for (int i = 0; i < S::RW - 1; ++i) v += slots[(rt * (S::RW - 1) + i) * 64 + lane];
+  for (int i = 0; i < S::kSlots; ++i)
+    if (i < S::RW - 1 || rt >= S::RW) v += slots[(rt * S::kSlots + i) * 64 + lane];
   return v;
 }
 
-// One row tile of V, dH or U: four values a lane.
+// One row tile of V, dH or U: four values a lane.  `rows` rows from `base`;
+// each row has a resource of its own, so that a lane keeps one offset.
 template <typename T>
 struct OneTile {
   uint32_t x[4];
-  __device__ __forceinline__ void load(const Slice<T>& s, int rt) {
-    int off = s.lane_off + 16 * rt * s.row_bytes;
+  __device__ __forceinline__ void load(const T* base, int ld, int rows, int rt, int io_off) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      if constexpr (sizeof(T) == 2) x[r] = __builtin_amdgcn_raw_buffer_load_b16(s.rsrc, off, 0, 0);
-      else x[r] = __builtin_amdgcn_raw_buffer_load_b32(s.rsrc, off, 0, 0);
-      off += s.row_bytes;
+      const int skip = 16 * rt + r, left = rows > skip ? rows - skip : 0;
+      const __amdgpu_buffer_rsrc_t b =
+          make_rsrc(base + (size_t)skip * ld, (uint32_t)__builtin_amdgcn_readfirstlane(left * ld * (int)sizeof(T)));
+      if constexpr (sizeof(T) == 2) x[r] = __builtin_amdgcn_raw_buffer_load_b16(b, 2 * io_off, 0, 0);
+      else x[r] = __builtin_amdgcn_raw_buffer_load_b32(b, 4 * io_off, 0, 0);
     }
   }
   __device__ __forceinline__ float4_t tile() const {
@@ -174,12 +171,12 @@ __device__ __forceinline__ void store_one(const Slice<float>& s, int rt, const f
 
 // FWD and TH as in delta_walk_kernel.
 template <typename TIn, typename TH, int DK, bool FWD>
-__global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_kernel(const DeltaParams p) {
+__global__ __launch_bounds__((64 * SplitShape<TIn, DK>::NW)) void delta_split_kernel(const DeltaParams p) {
   typedef SplitShape<TIn, DK> S;
-  constexpr int L = S::L, NP = S::NP, W = S::W, RT = S::RT, TS = S::TS, OWN = S::OWN, KT = W / 16;
+  constexpr int L = S::L, NP = S::NP, W = S::W, RT = S::RT, TS = S::TS, KT = W / 16;
   constexpr int PP = sizeof(TH) == 2 ? 2 : 3;
   __shared__ uint4 s_tiles[S::RW * (FWD ? 2 : 1) * S::kTile * 2 / 16];
-  __shared__ float4_t s_kc[RT * (S::RW - 1) * 64], s_qc[FWD ? RT * (S::RW - 1) * 64 : 1];
+  __shared__ float4_t s_kc[RT * S::kSlots * 64], s_qc[FWD ? RT * S::kSlots * 64 : 1];
   __shared__ uint4 s_x[TS * 3 * 64], s_wu[TS * 3 * 64], s_u[FWD ? TS * PP * 64 : 1];
   uint16_t* x_frags = reinterpret_cast<uint16_t*>(s_x);
   uint16_t* wu_frags = reinterpret_cast<uint16_t*>(s_wu);
@@ -189,7 +186,10 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ke
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, grp = lane >> 4;
   const int col = 16 * slice + row;
-  uint16_t* s_K = reinterpret_cast<uint16_t*>(s_tiles) + wave * (FWD ? 2 : 1) * S::kTile;
+  // row tile `wave` is this wave's; the first RW waves hold rows of the state
+  const int rt = wave;
+  const bool owner = S::RT == S::NW || wave < S::RT, holds = S::RW == S::NW || wave < S::RW;
+  uint16_t* s_K = reinterpret_cast<uint16_t*>(s_tiles) + (holds ? wave : 0) * (FWD ? 2 : 1) * S::kTile;
   uint16_t* s_Q = s_K + S::kTile;
   const TIn* K = static_cast<const TIn*>(p.K) + (size_t)bh * p.S * DK + wave * W;
   const TIn* Q = static_cast<const TIn*>(p.Q) + (size_t)bh * p.S * DK + wave * W;
@@ -201,46 +201,38 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ke
   float4_t C[KT];
 #pragma unroll
   for (int k = 0; k < KT; ++k) C[k] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-  if (p.C0) load_whole(Slice<float>(p.C0 + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), C);
+  if (p.C0 && holds) load_whole(Slice<float>(p.C0 + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), C);
 
   PartStage<TIn, DK, W, 64> gk, gq;
-  Parts<3> gt[OWN][TS];
-  Parts<PP> gp[OWN][TS];
-  OneTile<TIn> gv[OWN];
-  float4_t ge[OWN], gw[OWN];
+  Parts<3> gt[TS];
+  Parts<PP> gp[TS];
+  OneTile<TIn> gv;
+  float4_t ge, gw;
   float gg = 0.0f;
+  // The loads by where their registers are free again: K and Q once they are
+  // in LDS, the rest behind V - e K C, U and H.
   auto rows_of = [&](int c) { return p.S - c * L < L ? p.S - c * L : L; };
-  auto fetch_k = [&](int c) { gk.load(K + (size_t)c * L * DK, wave * W, rows_of(c), lane); };
-  auto fetch_q = [&](int c) {
-    if constexpr (FWD) gq.load(Q + (size_t)c * L * DK, wave * W, rows_of(c), lane);
+  auto row4_of = [&](const float* x, int c) {
+    return *reinterpret_cast<const float4_t*>(x + ((size_t)bh * p.Nc + c) * L + (owner ? 16 * rt + 4 * grp : 0));
   };
-  // by where their registers are free again: behind V - e K C, U and H
+  auto fetch_k = [&](int c) {
+    if (holds) gk.load(K + (size_t)c * L * DK, wave * W, rows_of(c), lane);
+  };
+  auto fetch_q = [&](int c) {
+    if constexpr (FWD)
+      if (holds) gq.load(Q + (size_t)c * L * DK, wave * W, rows_of(c), lane);
+  };
   auto fetch_v = [&](int c) {
-    const Slice<TIn> v(V + (size_t)c * L * p.DV, p.DV, rows_of(c), io_off);
-    const size_t at = (size_t)bh * p.Nc + c;
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int rt = own_tile<S>(wave, i);
-      gv[i].load(v, rt);
-      ge[i] = *reinterpret_cast<const float4_t*>(p.e + at * L + (rt < RT ? 16 * rt + 4 * grp : 0));
-    }
+    gv.load(V + (size_t)c * L * p.DV, p.DV, rows_of(c), rt, io_off);
+    ge = row4_of(p.e, c);
   };
   auto fetch_t = [&](int c) {
-    const size_t at = (size_t)bh * p.Nc + c;
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int rt = own_tile<S>(wave, i);
-      load_square_rows<L, false, 3>(p.T + at * kSquare, rt, gt[i], lane);
-      gw[i] = *reinterpret_cast<const float4_t*>(p.w + at * L + (rt < RT ? 16 * rt + 4 * grp : 0));
-    }
-    gg = p.e[at * L + L - 1];
+    load_square_rows<L, false, 3>(p.T + ((size_t)bh * p.Nc + c) * kSquare, rt, gt, lane);
+    gw = row4_of(p.w, c);
+    gg = p.e[((size_t)bh * p.Nc + c) * L + L - 1];
   };
   auto fetch_p = [&](int c) {
-    const size_t at = (size_t)bh * p.Nc + c;
-    if constexpr (FWD)
-#pragma unroll
-      for (int i = 0; i < OWN; ++i)
-        load_square_rows<L, false, PP>(p.P + at * kSquare, own_tile<S>(wave, i), gp[i], lane);
+    if constexpr (FWD) load_square_rows<L, false, PP>(p.P + ((size_t)bh * p.Nc + c) * kSquare, rt, gp, lane);
   };
   if (p.Nc) {
     fetch_k(0);
@@ -253,18 +245,17 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ke
   for (int c = 0; c < p.Nc; ++c) {
     const int t0 = c * L;
     const size_t at = (size_t)bh * p.Nc + c;
-    const int rows = rows_of(c);
-    gk.store(s_K, S::kPlane, lane);
-    if constexpr (FWD) gq.store(s_Q, S::kPlane, lane);
     const int next = c + 1 < p.Nc ? c + 1 : c;
-    __builtin_amdgcn_wave_barrier();
-    if constexpr (!FWD) store_whole(Slice<float>(p.C_states + (at * DK + wave * W) * p.DV, p.DV, W, io_off), C);
-
-    // this wave's share of K C and Q C
     float4_t kc[RT], qc[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) kc[rt] = qc[rt] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-    {
+    for (int j = 0; j < RT; ++j) kc[j] = qc[j] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    if (holds) {
+      gk.store(s_K, S::kPlane, lane);
+      if constexpr (FWD) gq.store(s_Q, S::kPlane, lane);
+      __builtin_amdgcn_wave_barrier();
+      if constexpr (!FWD) store_whole(Slice<float>(p.C_states + (at * DK + wave * W) * p.DV, p.DV, W, io_off), C);
+
+      // this wave's share of K C and Q C
       Parts<3> cp[W / 32];
       state_parts<W>(C, cp);
       part_rows_times<NP, W, 3>(s_K, S::kPlane, row_seed, cp, kc);
@@ -273,33 +264,27 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ke
         part_rows_times<NP, W, PP>(s_Q, S::kPlane, row_seed, cp, qc);
         send_shares<S>(s_qc, qc, wave, lane);
       }
-    }
 #pragma unroll
-    for (int k = 0; k < KT; ++k) C[k] *= gg;
+      for (int k = 0; k < KT; ++k) C[k] *= gg;
+    }
     fetch_k(next);
     __syncthreads();
 
     // the owners' tiles of V - e K C
-    float4_t h[OWN];
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int rt = own_tile<S>(wave, i);
-      if (rt >= RT) break;
-      put_operand<3>(x_frags, rt, gv[i].tile() - ge[i] * take_shares<S>(s_kc, kc, rt, lane), lane);
-      if constexpr (FWD) h[i] = ge[i] * take_shares<S>(s_qc, qc, rt, lane);
+    float4_t h = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (owner) {
+      put_operand<3>(x_frags, rt, gv.tile() - ge * take_shares<S>(s_kc, kc, rt, lane), lane);
+      if constexpr (FWD) h = ge * take_shares<S>(s_qc, qc, rt, lane);
     }
     fetch_v(next);
     fetch_q(next);
     __syncthreads();
 
     // ... and of U
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int rt = own_tile<S>(wave, i);
-      if (rt >= RT) break;
+    if (owner) {
       float4_t u = {0.0f, 0.0f, 0.0f, 0.0f};
-      tile_times<L, false, 3, 3>(gt[i], x_frags, rt, u, lane);
-      put_operand<3>(wu_frags, rt, gw[i] * u, lane);
+      tile_times<L, false, 3, 3>(gt, x_frags, rt, u, lane);
+      put_operand<3>(wu_frags, rt, gw * u, lane);
       if constexpr (FWD) put_operand<PP>(u_frags, rt, u, lane);
       else store_one(Slice<float>(p.U + at * L * p.DV, p.DV, L, io_off), rt, u);
     }
@@ -307,39 +292,38 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ke
     __syncthreads();
 
     // C <- g C + K^T (w U), H = s (e Q C + P U)
+    if (holds) {
 #pragma unroll
-    for (int ts = 0; ts < TS; ++ts) {
-      const Parts<3> wu = lds_row8<3>(wu_frags + ts * 3 * kFragElems + 8 * lane, kFragElems);
+      for (int ts = 0; ts < TS; ++ts) {
+        const Parts<3> wu = lds_row8<3>(wu_frags + ts * 3 * kFragElems + 8 * lane, kFragElems);
 #pragma unroll
-      for (int k = 0; k < KT; ++k)
-        C[k] = mma_parts<NP, 3>(tile_col<NP, W>(s_K, S::kPlane, col_seed, ts, k), wu, C[k]);
+        for (int k = 0; k < KT; ++k)
+          C[k] = mma_parts<NP, 3>(tile_col<NP, W>(s_K, S::kPlane, col_seed, ts, k), wu, C[k]);
+      }
     }
     if constexpr (FWD) {
-      const Slice<TH> out(static_cast<TH*>(p.H) + ((size_t)bh * p.S + t0) * p.DV, p.DV, rows, io_off);
-#pragma unroll
-      for (int i = 0; i < OWN; ++i) {
-        const int rt = own_tile<S>(wave, i);
-        if (rt >= RT) break;
-        tile_times<L, false, PP, PP>(gp[i], u_frags, rt, h[i], lane);
-        store_tile(out, rt, h[i], p.scale, lane);
+      if (owner) {
+        tile_times<L, false, PP, PP>(gp, u_frags, rt, h, lane);
+        store_tile(Slice<TH>(static_cast<TH*>(p.H) + ((size_t)bh * p.S + t0) * p.DV, p.DV, rows_of(c), io_off), rt, h,
+                   p.scale, lane);
       }
     }
     fetch_p(next);
   }
 
-  if (p.C_out) store_whole(Slice<float>(p.C_out + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), C);
+  if (p.C_out && holds) store_whole(Slice<float>(p.C_out + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), C);
 }
 
 // The backward walk in the same form; formulas and outputs as in
 // delta_walk_back_kernel, whose anchor slots hold one sum per sixteen columns.
 template <typename TIn, typename TH, int DK>
-__global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_back_kernel(const DeltaParams p) {
+__global__ __launch_bounds__((64 * SplitShape<TIn, DK>::NW)) void delta_split_back_kernel(const DeltaParams p) {
   typedef SplitShape<TIn, DK> S;
-  constexpr int L = S::L, NP = S::NP, W = S::W, RT = S::RT, TS = S::TS, OWN = S::OWN, KT = W / 16;
+  constexpr int L = S::L, NP = S::NP, W = S::W, RT = S::RT, TS = S::TS, KT = W / 16;
   __shared__ uint4 s_tiles[S::RW * 2 * S::kTile * 2 / 16];
-  __shared__ float4_t s_kg[RT * (S::RW - 1) * 64];
+  __shared__ float4_t s_kg[RT * S::kSlots * 64];
   __shared__ uint4 s_h[TS * 3 * 64], s_eh[TS * 3 * 64], s_du[TS * 3 * 64], s_dv[TS * 3 * 64];
-  __shared__ float s_anchor[2][S::RW];
+  __shared__ float s_anchor[2][RT];
   uint16_t* h_frags = reinterpret_cast<uint16_t*>(s_h);
   uint16_t* eh_frags = reinterpret_cast<uint16_t*>(s_eh);
   uint16_t* du_frags = reinterpret_cast<uint16_t*>(s_du);
@@ -349,7 +333,10 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ba
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, grp = lane >> 4;
   const int col = 16 * slice + row;
-  uint16_t* s_K = reinterpret_cast<uint16_t*>(s_tiles) + wave * 2 * S::kTile;
+  // row tile `wave` is this wave's; the first RW waves hold rows of the state
+  const int rt = wave;
+  const bool owner = S::RT == S::NW || wave < S::RT, holds = S::RW == S::NW || wave < S::RW;
+  uint16_t* s_K = reinterpret_cast<uint16_t*>(s_tiles) + (holds ? wave : 0) * 2 * S::kTile;
   uint16_t* s_Q = s_K + S::kTile;
   const TIn* K = static_cast<const TIn*>(p.K) + (size_t)bh * p.S * DK + wave * W;
   const TIn* Q = static_cast<const TIn*>(p.Q) + (size_t)bh * p.S * DK + wave * W;
@@ -361,44 +348,37 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ba
   float4_t G[KT];
 #pragma unroll
   for (int k = 0; k < KT; ++k) G[k] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-  if (p.dC_out) load_whole(Slice<float>(p.dC_out + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), G);
+  if (p.dC_out && holds) load_whole(Slice<float>(p.dC_out + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), G);
 
   PartStage<TIn, DK, W, 64> gk, gq;
-  Parts<3> gt[OWN][TS], gp[OWN][TS];
-  OneTile<TH> gh[OWN];
-  OneTile<float> gu[OWN];
-  float4_t ge[OWN], gw[OWN];
+  Parts<3> gt[TS], gp[TS];
+  OneTile<TH> gh;
+  OneTile<float> gu;
+  float4_t ge, gw;
   float gg = 0.0f;
   auto rows_of = [&](int c) { return p.S - c * L < L ? p.S - c * L : L; };
-  auto fetch_k = [&](int c) { gk.load(K + (size_t)c * L * DK, wave * W, rows_of(c), lane); };
-  auto fetch_q = [&](int c) { gq.load(Q + (size_t)c * L * DK, wave * W, rows_of(c), lane); };
+  auto row4_of = [&](const float* x, int c) {
+    return *reinterpret_cast<const float4_t*>(x + ((size_t)bh * p.Nc + c) * L + (owner ? 16 * rt + 4 * grp : 0));
+  };
+  auto fetch_k = [&](int c) {
+    if (holds) gk.load(K + (size_t)c * L * DK, wave * W, rows_of(c), lane);
+  };
+  auto fetch_q = [&](int c) {
+    if (holds) gq.load(Q + (size_t)c * L * DK, wave * W, rows_of(c), lane);
+  };
   auto fetch_h = [&](int c) {
-    const size_t at = (size_t)bh * p.Nc + c;
-    const Slice<TH> h(dH + (size_t)c * L * p.DV, p.DV, rows_of(c), io_off);
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int rt = own_tile<S>(wave, i);
-      gh[i].load(h, rt);
-      ge[i] = *reinterpret_cast<const float4_t*>(p.e + at * L + (rt < RT ? 16 * rt + 4 * grp : 0));
-    }
-    gg = p.e[at * L + L - 1];
+    gh.load(dH + (size_t)c * L * p.DV, p.DV, rows_of(c), rt, io_off);
+    ge = row4_of(p.e, c);
+    gg = p.e[((size_t)bh * p.Nc + c) * L + L - 1];
   };
   auto fetch_p = [&](int c) {
     const size_t at = (size_t)bh * p.Nc + c;
-    const Slice<float> u(p.U + at * L * p.DV, p.DV, L, io_off);
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int rt = own_tile<S>(wave, i);
-      load_square_rows<L, true, 3>(p.P + at * kSquare, rt, gp[i], lane);
-      gu[i].load(u, rt);
-      gw[i] = *reinterpret_cast<const float4_t*>(p.w + at * L + (rt < RT ? 16 * rt + 4 * grp : 0));
-    }
+    load_square_rows<L, true, 3>(p.P + at * kSquare, rt, gp, lane);
+    gu.load(p.U + at * L * p.DV, p.DV, L, rt, io_off);
+    gw = row4_of(p.w, c);
   };
   auto fetch_t = [&](int c) {
-    const size_t at = (size_t)bh * p.Nc + c;
-#pragma unroll
-    for (int i = 0; i < OWN; ++i)
-      load_square_rows<L, true, 3>(p.Tt + at * kSquare, own_tile<S>(wave, i), gt[i], lane);
+    load_square_rows<L, true, 3>(p.Tt + ((size_t)bh * p.Nc + c) * kSquare, rt, gt, lane);
   };
   if (p.Nc) {
     fetch_h(p.Nc - 1);
@@ -411,104 +391,96 @@ __global__ __launch_bounds__((64 * SplitShape<TIn, DK>::RW)) void delta_split_ba
   for (int c = p.Nc - 1; c >= 0; --c) {
     const int t0 = c * L;
     const size_t at = (size_t)bh * p.Nc + c;
-    const int rows = rows_of(c);
-    gk.store(s_K, S::kPlane, lane);
-    gq.store(s_Q, S::kPlane, lane);
-    float4_t e[OWN];
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      e[i] = ge[i];
-      const int rt = own_tile<S>(wave, i);
-      if (rt >= RT) continue;
-      const float4_t h = p.scale * gh[i].tile();
-      put_operand<3>(h_frags, rt, h, lane);
-      put_operand<3>(eh_frags, rt, e[i] * h, lane);
-    }
-    const float g = gg;
     const int next = c > 0 ? c - 1 : c;
-    __builtin_amdgcn_wave_barrier();
-    store_whole(Slice<float>(p.G_states + (at * DK + wave * W) * p.DV, p.DV, W, io_off), G);
-
-    // this wave's share of K G
+    const float4_t e = ge;
+    if (owner) {
+      const float4_t h = p.scale * gh.tile();
+      put_operand<3>(h_frags, rt, h, lane);
+      put_operand<3>(eh_frags, rt, e * h, lane);
+    }
     float4_t kg[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) kg[rt] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-    {
+    for (int j = 0; j < RT; ++j) kg[j] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    if (holds) {
+      gk.store(s_K, S::kPlane, lane);
+      gq.store(s_Q, S::kPlane, lane);
+      __builtin_amdgcn_wave_barrier();
+      store_whole(Slice<float>(p.G_states + (at * DK + wave * W) * p.DV, p.DV, W, io_off), G);
+
+      // this wave's share of K G
       Parts<3> gs[W / 32];
       state_parts<W>(G, gs);
       part_rows_times<NP, W, 3>(s_K, S::kPlane, row_seed, gs, kg);
       send_shares<S>(s_kg, kg, wave, lane);
-    }
 #pragma unroll
-    for (int k = 0; k < KT; ++k) G[k] *= g;
+      for (int k = 0; k < KT; ++k) G[k] *= gg;
+    }
     fetch_h(next);
     fetch_k(next);
     __syncthreads();
 
     // the owners' tiles of dU = s P^T dH + w K G
     float anchor = 0.0f;
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int rt = own_tile<S>(wave, i);
-      if (rt >= RT) break;
-      const float4_t u = gu[i].tile();
-      float4_t du = gw[i] * take_shares<S>(s_kg, kg, rt, lane);
+    if (owner) {
+      const float4_t u = gu.tile();
+      float4_t du = gw * take_shares<S>(s_kg, kg, rt, lane);
 #pragma unroll
       for (int r = 0; r < 4; ++r) anchor += du[r] * u[r];
-      tile_times<L, true, 3, 3>(gp[i], h_frags, rt, du, lane);
+      tile_times<L, true, 3, 3>(gp, h_frags, rt, du, lane);
       put_operand<3>(du_frags, rt, du, lane);
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) anchor += __shfl_xor(anchor, o, 64);
-    if (lane == 0) s_anchor[c & 1][wave] = anchor;
     fetch_q(next);
     fetch_p(next);
     __syncthreads();
 
     // ... and of dV = T^T dU
-    const Slice<TIn> out(static_cast<TIn*>(p.dV) + ((size_t)bh * p.S + t0) * p.DV, p.DV, rows, io_off);
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int rt = own_tile<S>(wave, i);
-      if (rt >= RT) break;
+    if (owner) {
       float4_t dv = {0.0f, 0.0f, 0.0f, 0.0f};
-      tile_times<L, true, 3, 3>(gt[i], du_frags, rt, dv, lane);
-      put_operand<3>(dv_frags, rt, -e[i] * dv, lane);
+      tile_times<L, true, 3, 3>(gt, du_frags, rt, dv, lane);
+      put_operand<3>(dv_frags, rt, -e * dv, lane);
       store_one(Slice<float>(p.R + at * L * p.DV, p.DV, L, io_off), rt, dv);
-      store_tile(out, rt, dv, 1.0f, lane);
+      store_tile(Slice<TIn>(static_cast<TIn*>(p.dV) + ((size_t)bh * p.S + t0) * p.DV, p.DV, rows_of(c), io_off), rt, dv,
+                 1.0f, lane);
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) anchor += __shfl_xor(anchor, o, 64);
+      if (lane == 0) s_anchor[c & 1][wave] = anchor;
+    }
+
+    // G <- g G + Q^T (s e dH), before the barrier that dV needs, and - K^T (e dV)
+    if (holds) {
+#pragma unroll
+      for (int ts = 0; ts < TS; ++ts) {
+        const Parts<3> h = lds_row8<3>(eh_frags + ts * 3 * kFragElems + 8 * lane, kFragElems);
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+          G[k] = mma_parts<NP, 3>(tile_col<NP, W>(s_Q, S::kPlane, col_seed, ts, k), h, G[k]);
+      }
+    }
+    fetch_t(next);
+    __syncthreads();
+    if (holds) {
+#pragma unroll
+      for (int ts = 0; ts < TS; ++ts) {
+        const Parts<3> d = lds_row8<3>(dv_frags + ts * 3 * kFragElems + 8 * lane, kFragElems);
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+          G[k] = mma_parts<NP, 3>(tile_col<NP, W>(s_K, S::kPlane, col_seed, ts, k), d, G[k]);
+      }
     }
     if (threadIdx.x == 0) {
       float a = 0.0f;
 #pragma unroll
-      for (int i = 0; i < S::RW; ++i) a += s_anchor[c & 1][i];
+      for (int i = 0; i < RT; ++i) a += s_anchor[c & 1][i];
       p.anchor[at * (p.DV / 16) + slice] = a;
-    }
-
-    // G <- g G + Q^T (s e dH), before the barrier that dV needs, and - K^T (e dV)
-#pragma unroll
-    for (int ts = 0; ts < TS; ++ts) {
-      const Parts<3> h = lds_row8<3>(eh_frags + ts * 3 * kFragElems + 8 * lane, kFragElems);
-#pragma unroll
-      for (int k = 0; k < KT; ++k)
-        G[k] = mma_parts<NP, 3>(tile_col<NP, W>(s_Q, S::kPlane, col_seed, ts, k), h, G[k]);
-    }
-    fetch_t(next);
-    __syncthreads();
-#pragma unroll
-    for (int ts = 0; ts < TS; ++ts) {
-      const Parts<3> d = lds_row8<3>(dv_frags + ts * 3 * kFragElems + 8 * lane, kFragElems);
-#pragma unroll
-      for (int k = 0; k < KT; ++k)
-        G[k] = mma_parts<NP, 3>(tile_col<NP, W>(s_K, S::kPlane, col_seed, ts, k), d, G[k]);
     }
   }
 
-  if (p.dC0) store_whole(Slice<float>(p.dC0 + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), G);
+  if (p.dC0 && holds) store_whole(Slice<float>(p.dC0 + ((size_t)bh * DK + wave * W) * p.DV, p.DV, W, io_off), G);
 }
 
 template <typename TIn, typename TH, int DK>
 hipError_t launch_dk(const DeltaParams& p, DeltaWalk what, hipStream_t stream) {
-  const dim3 grid((unsigned)((long long)p.BH * (p.DV / 16))), block(64 * SplitShape<TIn, DK>::RW);
+  const dim3 grid((unsigned)((long long)p.BH * (p.DV / 16))), block(64 * SplitShape<TIn, DK>::NW);
   switch (what) {
     case DeltaWalk::kForward:
       hipLaunchKernelGGL((delta_split_kernel<TIn, TH, DK, true>), grid, block, 0, stream, p);
