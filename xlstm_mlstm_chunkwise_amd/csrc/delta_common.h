@@ -57,9 +57,10 @@ __device__ __forceinline__ Parts<N> split_parts(const float (&x)[8]) {
   return f;
 }
 
-// Four floats as N parts, two words each.
+// Four floats as N parts, two words each.  (Words as native vectors: arrays of
+// HIP's uint2 end up in memory.)
 template <int N>
-__device__ __forceinline__ void split4(const float4_t& x, uint2 (&w)[N]) {
+__device__ __forceinline__ void split4(const float4_t& x, words2_t (&w)[N]) {
   if constexpr (N == 3) {
     float a[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -67,15 +68,27 @@ __device__ __forceinline__ void split4(const float4_t& x, uint2 (&w)[N]) {
       uint32_t u[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(a[e]);
-      w[n] = make_uint2(__builtin_amdgcn_perm(u[1], u[0], 0x07060302u), __builtin_amdgcn_perm(u[3], u[2], 0x07060302u));
+      w[n] = (words2_t){__builtin_amdgcn_perm(u[1], u[0], 0x07060302u), __builtin_amdgcn_perm(u[3], u[2], 0x07060302u)};
 #pragma unroll
       for (int e = 0; e < 4; ++e) a[e] -= __uint_as_float(u[e] & 0xffff0000u);
     }
   } else {
     static_assert(N == 2, "two or three parts");
-    split_bf16x2(x[0], x[1], w[0].x, w[1].x);
-    split_bf16x2(x[2], x[3], w[0].y, w[1].y);
+    uint32_t h0, l0, h1, l1;
+    split_bf16x2(x[0], x[1], h0, l0);
+    split_bf16x2(x[2], x[3], h1, l1);
+    w[0] = (words2_t){h0, h1};
+    w[1] = (words2_t){l0, l1};
   }
+}
+
+// The same eight values' parts from two split halves.
+__device__ __forceinline__ Parts<3> join_halves(const words2_t (&a)[3], const words2_t (&b)[3]) {
+  Parts<3> f;
+#pragma unroll
+  for (int n = 0; n < 3; ++n)
+    f.p[n] = __builtin_bit_cast(bf16x8_t, (words4_t){a[n][0], a[n][1], b[n][0], b[n][1]});
+  return f;
 }
 
 template <int N, int M>

@@ -95,10 +95,10 @@ struct Quad {
 
 template <int N>
 __device__ __forceinline__ void store_quads(uint16_t* p, int plane, const float4_t& x) {
-  uint2 w[N];
+  words2_t w[N];
   split4<N>(x, w);
 #pragma unroll
-  for (int n = 0; n < N; ++n) *reinterpret_cast<uint2*>(p + n * plane) = w[n];
+  for (int n = 0; n < N; ++n) *reinterpret_cast<words2_t*>(p + n * plane) = w[n];
 }
 
 template <typename TIn, typename TH, int DK>

@@ -38,11 +38,11 @@ struct SplitShape {
 // its 32-row block, N parts.
 template <int N>
 __device__ __forceinline__ void put_operand(uint16_t* frags, int rt, const float4_t& x, int lane) {
-  uint2 w[N];
+  words2_t w[N];
   split4<N>(x, w);
 #pragma unroll
   for (int n = 0; n < N; ++n)
-    *reinterpret_cast<uint2*>(frags + ((rt >> 1) * N + n) * kFragElems + 8 * lane + 4 * (rt & 1)) = w[n];
+    *reinterpret_cast<words2_t*>(frags + ((rt >> 1) * N + n) * kFragElems + 8 * lane + 4 * (rt & 1)) = w[n];
 }
 
 // acc += row tile rt of M (UP: of M^T) . X, fragments of M in registers and of

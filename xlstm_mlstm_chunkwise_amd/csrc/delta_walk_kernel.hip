@@ -112,25 +112,29 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
-        C[2 * ks] *= g;
-        C[2 * ks + 1] *= g;
+        const bool more = ks + 1 < DK / 32;
+        words2_t lo[3] = {}, hi[3] = {};
         if constexpr (FWD) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) next[rt] = tile_row<NP, DK>(s_Q, W::kPlane, row_seed, rt, ks);
+          if (more) split4<3>(C[2 * ks + 2], lo);
           rows_times(f, cp, kc);
-          end_step<2 * NP * RT, RT * mma_count<NP, 3>(), 1>();
+          end_step<2 * NP * RT, RT * mma_count<NP, 3>(), 2>();
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) f[rt] = next[rt];
         }
-        if (ks + 1 < DK / 32) {
+        C[2 * ks] *= g;
+        C[2 * ks + 1] *= g;
+        if (more) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) next[rt] = tile_row<NP, DK>(s_K, W::kPlane, row_seed, rt, ks + 1);
-          tiles8(C[2 * ks + 2], C[2 * ks + 3], x);
-          cn = split_parts<3>(x);
+          if constexpr (!FWD) split4<3>(C[2 * ks + 2], lo);
+          split4<3>(C[2 * ks + 3], hi);
+          cn = join_halves(lo, hi);
         }
         if constexpr (FWD) rows_times(f, first_parts<PP>(cp), qc);
         else rows_times(f, cp, kc);
-        if (ks + 1 < DK / 32) end_step<2 * NP * RT, RT * (FWD ? mma_count<NP, PP>() : mma_count<NP, 3>()), FWD ? 6 : 4>();
+        if (more) end_step<2 * NP * RT, RT * (FWD ? mma_count<NP, PP>() : mma_count<NP, 3>()), 4>();
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) f[rt] = next[rt];
         cp = cn;
