@@ -22,6 +22,9 @@ struct WalkLds {
   static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts, NF = square_frags<L>();
   static constexpr int kPlane = L * DK;
   static constexpr int kBytes = 2 * (2 * NP * kPlane + NF * (3 + PP) * kFragElems) + 4 * 2 * L;
+  // two buffers of everything but Q (PP = 0: no Q and no P)
+  static constexpr int kTwice = 2 * ((PP ? 3 : 2) * NP * kPlane + 2 * NF * (3 + PP) * kFragElems) + 4 * 4 * L;
+  static constexpr bool kDouble = kTwice <= 160 * 1024;
 };
 
 // FWD: H (type TH) and the final state.  !FWD: the state entering every chunk
@@ -32,13 +35,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
   constexpr int PP = sizeof(TH) == 2 ? 2 : 3;
   typedef WalkLds<TIn, DK, FWD ? PP : 0> W;
   constexpr int L = W::L, NP = W::NP, RT = L / 16, TS = L / 32, KT = DK / 16, THREADS = 64 * NW;
-  __shared__ uint4 smem[W::kBytes / 16];
-  uint16_t* s_K = reinterpret_cast<uint16_t*>(smem);
-  uint16_t* s_Q = s_K + NP * W::kPlane;
-  uint16_t* s_T = s_Q + NP * W::kPlane;
-  uint16_t* s_P = s_T + W::NF * 3 * kFragElems;
-  float* s_e = reinterpret_cast<float*>(s_P + (FWD ? W::NF * PP * kFragElems : 0));
-  float* s_w = s_e + L;
+  // With two buffers the next chunk's tiles are stored while this one is still
+  // read, under the last products; Q, which only the first phase reads, needs
+  // one, freed by a barrier behind that phase.
+  constexpr bool DB = W::kDouble;
+  constexpr int BUFS = DB ? 2 : 1, kTileK = NP * W::kPlane, kFragT = W::NF * 3 * kFragElems;
+  constexpr int kFragP = FWD ? W::NF * PP * kFragElems : 0;
+  __shared__ uint4 smem[(DB ? W::kTwice : W::kBytes) / 16];
+  uint16_t* const m_K = reinterpret_cast<uint16_t*>(smem);
+  uint16_t* const s_Q = m_K + BUFS * kTileK;
+  uint16_t* const m_T = s_Q + (FWD || !DB ? kTileK : 0);
+  uint16_t* const m_P = m_T + BUFS * kFragT;
+  float* const m_e = reinterpret_cast<float*>(m_P + BUFS * kFragP);
 
   // slices of one head share an XCD's L2 where the head count is a multiple of 8
   const int bh = blockIdx.x % p.BH, slice = blockIdx.x / p.BH;
@@ -70,22 +78,37 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     if constexpr (FWD) gp.load(p.P + at * kSquare, tid);
     if (tid < 2 * L) ge = tid < L ? p.e[at * L + tid] : p.w[at * L + tid - L];
   };
-  if (p.Nc) fetch(0);
+  auto store = [&](int buf, int part) {
+    if (part == 0) gk.store(m_K + buf * kTileK, W::kPlane, tid);
+    if (FWD && part == 1) gq.store(s_Q, W::kPlane, tid);
+    if (part == 2) gt.store(m_T + buf * kFragT, tid);
+    if (FWD && part == 3) gp.store(m_P + buf * kFragP, tid);
+    if (part == 3 && tid < 2 * L) m_e[buf * 2 * L + tid] = ge;
+  };
+  if (p.Nc) {
+    fetch(0);
+    if (DB)
+      for (int i = 0; i < 4; ++i) store(0, i);
+  }
 
   for (int c = 0; c < p.Nc; ++c) {
-    const int t0 = c * L;
+    const int t0 = c * L, buf = DB ? c & 1 : 0, next = c + 1 < p.Nc ? c + 1 : c;
     const size_t at = (size_t)bh * p.Nc + c;
+    const uint16_t* s_K = m_K + buf * kTileK;
+    const uint16_t* s_T = m_T + buf * kFragT;
+    const uint16_t* s_P = m_P + buf * kFragP;
+    const float* s_e = m_e + buf * 2 * L;
+    const float* s_w = s_e + L;
     keep_in_loop(row_seed);
     keep_in_loop(col_seed);
     keep_in_loop(io_off);
-    __syncthreads();  // the chunk before is read out
-    gk.store(s_K, W::kPlane, tid);
-    if constexpr (FWD) gq.store(s_Q, W::kPlane, tid);
-    gt.store(s_T, tid);
-    if constexpr (FWD) gp.store(s_P, tid);
-    if (tid < 2 * L) s_e[tid] = ge;
-    __syncthreads();
-    if (c + 1 < p.Nc) fetch(c + 1);
+    __syncthreads();  // the chunk before is read out (two buffers: and this one stored)
+    if constexpr (!DB) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store(0, i);
+      __syncthreads();
+      fetch(next);
+    }
     RawTiles<TIn, RT> v;
     const int rows = p.S - t0 < L ? p.S - t0 : L;
     v.load(Slice<TIn>(V + (size_t)t0 * p.DV, p.DV, rows, io_off));
@@ -141,6 +164,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
       }
     }
 
+    if constexpr (DB) {
+      if constexpr (FWD) __syncthreads();  // Q is read out
+      fetch(next);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+
     // U = T (V - e K C)
     float4_t u[RT];
     {
@@ -188,6 +217,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
       tile_cols_times<NP, DK, 3>(s_K, W::kPlane, col_seed, ts, wp[ts], C, [&](int i) {
         const int rt = ts * (DK / 32) + i;
         if (FWD && rt < RT) store_tile(out, rt, qc[rt], p.scale, lane);
+        if (DB && ts == TS - 1)
+#pragma unroll
+          for (int part = 0; part < 4; ++part)
+            if (i == (part < DK / 32 ? part : DK / 32 - 1)) store(buf ^ 1, part);
       });
   }
 
