@@ -997,11 +997,20 @@ def head_norm_bw(x, dy, weight=None, *, eps: float = 1e-6, weight_grads: bool = 
     dev = x.device
     _check_on(dev, "dy", dy, (B, S, NH, D), dy.dtype)
     _check_on(dev, "weight", weight, (NH, D), torch.float32)
+    return _norm_grads(x, dy, weight, eps, weight_grads, weight_grads, workspace)
+
+
+def _norm_grads(x, dy, weight, eps, weight_grad, bias_grad, workspace=None):
+    """head_norm_bw for checked inputs, with either of the two sums left out."""
+    torch = _torch()
+    B, NH, S, D = x.shape
+    dev = x.device
     desc, need = _norm_plan("mlstm_head_norm_bw", B, NH, S, D, x.dtype, dy.dtype, eps)
-    dx, dw, db, ws_bytes = torch.empty_like(x), None, None, 0
-    if weight_grads:
+    dx, ws_bytes = torch.empty_like(x), 0
+    dw = torch.empty((NH, D), dtype=torch.float32, device=dev) if weight_grad else None
+    db = torch.empty((NH, D), dtype=torch.float32, device=dev) if bias_grad else None
+    if weight_grad or bias_grad:
         workspace, ws_bytes = _bytes_of(need, workspace, dev)
-        dw, db = (torch.empty((NH, D), dtype=torch.float32, device=dev) for _ in range(2))
     _call("mlstm_head_norm_bw", dev, desc, _ptr(x), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
           _ptr(workspace), ws_bytes)
     return dx, dw, db
@@ -1022,9 +1031,9 @@ def _head_norm_function():
             @torch.autograd.function.once_differentiable
             def backward(ctx, dy):
                 x, weight = ctx.saved_tensors
-                need = ctx.needs_input_grad
-                dx, dw, db = head_norm_bw(x, dy.contiguous(), weight, eps=ctx.eps, weight_grads=need[1] or need[2])
-                return dx, dw if need[1] else None, db if need[2] else None, None, None
+                _, need_w, need_b, _, _ = ctx.needs_input_grad
+                # the forward has checked x and weight, and dy has y's shape and type
+                return (*_norm_grads(x, dy.contiguous(), weight, ctx.eps, need_w, need_b), None, None)
 
         _functions["norm"] = HeadNorm
     return _functions["norm"]

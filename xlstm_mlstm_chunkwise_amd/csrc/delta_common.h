@@ -192,10 +192,6 @@ struct DeltaIn<float> {
   static constexpr int kParts = 3, kChunk = kDeltaChunkF32;
 };
 
-__device__ __forceinline__ float load1(const bf16_t* p) { return bf16_to_f32(p->bits); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ void store1(bf16_t* p, float x) { p->bits = f32_to_bf16(x); }
-__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store4(bf16_t* p, float a, float b, float c, float d) {
   *reinterpret_cast<uint2*>(p) = make_uint2(round_bf16x2(a, b), round_bf16x2(c, d));
 }

@@ -17,23 +17,23 @@ namespace {
 
 typedef float nt_f4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kRowGroups = 16;
+constexpr int kRowGroups = 16, kCols = 64, kThreads = kCols / 4 * kRowGroups;
 
 __device__ __forceinline__ float ld(const void* x, size_t i, int bf16) {
   return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(x)[i]) : static_cast<const float*>(x)[i];
 }
 
-template <int DK, int COLS>
-__global__ __launch_bounds__(COLS / 4 * kRowGroups) void delta_step_kernel(const DeltaStepParams p) {
-  constexpr int THREADS = COLS / 4 * kRowGroups, RPT = DK / kRowGroups, CQ = COLS / 4;
-  __shared__ float s_q[DK], s_k[DK], s_kq[THREADS / 64];
+template <int DK>
+__global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaStepParams p) {
+  constexpr int RPT = DK / kRowGroups, CQ = kCols / 4;
+  __shared__ float s_q[DK], s_k[DK], s_kq[kThreads / 64];
   __shared__ float4 s_ck[kRowGroups][CQ], s_cq[kRowGroups][CQ];
   __shared__ float4 s_u[CQ];
 
-  const int NS = p.DV / COLS;
+  const int NS = p.DV / kCols;
   const int bh = blockIdx.x / NS, slice = blockIdx.x % NS;
   const int tid = threadIdx.x, cq = tid % CQ, rg = tid / CQ;
-  const int col = slice * COLS + 4 * cq;
+  const int col = slice * kCols + 4 * cq;
   const size_t base = (size_t)bh * DK * p.DV + col;
 
   nt_f4_t C[RPT];
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(COLS / 4 * kRowGroups) void delta_step_kernel(const
   const float a = expf(log_sigmoid(p.f_pre[bh]));
   const float b = 1.0f / (1.0f + expf(-p.i_pre[bh]));
   float dot = 0.0f;
-  for (int i = tid; i < DK; i += THREADS) {
+  for (int i = tid; i < DK; i += kThreads) {
     const float q = ld(p.q, (size_t)bh * DK + i, p.qkv_bf16), k = ld(p.k, (size_t)bh * DK + i, p.qkv_bf16);
     s_q[i] = q;
     s_k[i] = k;
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(COLS / 4 * kRowGroups) void delta_step_kernel(const
   if (rg == 0) {
     float kq = 0.0f;
 #pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w) kq += s_kq[w];
+    for (int w = 0; w < kThreads / 64; ++w) kq += s_kq[w];
 #pragma unroll
     for (int g = 1; g < kRowGroups; ++g) {
       const nt_f4_t x = __builtin_bit_cast(nt_f4_t, s_ck[g][cq]), y = __builtin_bit_cast(nt_f4_t, s_cq[g][cq]);
@@ -115,10 +115,8 @@ __global__ __launch_bounds__(COLS / 4 * kRowGroups) void delta_step_kernel(const
 
 template <int DK>
 hipError_t launch_dk(const DeltaStepParams& p, hipStream_t stream) {
-  const int cols = p.DV % 128 == 0 ? 128 : 64;
-  const dim3 grid((unsigned)((long long)p.BH * (p.DV / cols))), block(cols / 4 * kRowGroups);
-  if (cols == 128) hipLaunchKernelGGL((delta_step_kernel<DK, 128>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((delta_step_kernel<DK, 64>), grid, block, 0, stream, p);
+  const dim3 grid((unsigned)((long long)p.BH * (p.DV / kCols))), block(kThreads);
+  hipLaunchKernelGGL((delta_step_kernel<DK>), grid, block, 0, stream, p);
   return hipGetLastError();
 }
 

@@ -22,11 +22,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void load8f(const void* p, size_t i, bool bf16, float (&x)[8]) {
-  if (bf16) Ops<bf16_t>::load8(static_cast<const bf16_t*>(p) + i, x);
-  else Ops<float>::load8(static_cast<const float*>(p) + i, x);
-}
-
 template <typename T>
 __device__ __forceinline__ void store8f(T* p, const float (&x)[8]) {
   store4(p, x[0], x[1], x[2], x[3]);
@@ -38,11 +33,24 @@ __device__ __forceinline__ void store8f<bf16_t>(bf16_t* p, const float (&x)[8]) 
                                             round_bf16x2(x[4], x[5]), round_bf16x2(x[6], x[7]));
 }
 
-// Sum over the LPR lanes of a row.
+// Sum over the LPR lanes of a row, in every lane, without LDS: within sixteen
+// lanes by quad permutes and mirrors, across them by row swaps (of a value
+// with itself: each half of the result holds one operand of the sum).
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+  auto plus = [&](auto moved) { x += __int_as_float(moved(__float_as_int(x))); };
+  plus([](int v) { return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true); });   // lane ^ 1
+  plus([](int v) { return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true); });   // lane ^ 2
+  plus([](int v) { return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true); });  // the other quad of eight
+  if constexpr (LPR >= 16) plus([](int v) { return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true); });
+  if constexpr (LPR >= 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  if constexpr (LPR == 64) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
   return x;
 }
 
@@ -65,32 +73,69 @@ __device__ __forceinline__ float normalise(float (&x)[8], bool in, float inv_d, 
   return rstd;
 }
 
-template <typename TX, typename TY, int LPR>
+// Eight values a lane as they are in memory: they become floats where they are
+// used, so that nothing waits for the loads before.
+template <typename T>
+struct Raw8 {
+  words4_t w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, bool in) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      w[i] = (words4_t){0u, 0u, 0u, 0u};
+      if (in) w[i] = reinterpret_cast<const words4_t*>(p)[i];
+    }
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(T) == 2)
+        x[e] = __uint_as_float(e % 2 ? w[0][e / 2] & 0xffff0000u : w[0][e / 2] << 16);
+      else
+        x[e] = __uint_as_float(w[e / 4][e % 4]);
+    }
+  }
+};
+
+// R rows one after another: their loads go out together, and a head's weight
+// and bias (64 bytes a lane against a bf16 row's 16) are read once for them.
+template <typename TX, typename TY, int LPR, int R>
 __global__ __launch_bounds__(kThreads) void head_norm_kernel(const HeadNormParams p) {
-  constexpr int RPB = kThreads / LPR;  // rows a workgroup
-  const long long r = (long long)blockIdx.x * RPB + threadIdx.x / LPR;
+  constexpr int RPB = kThreads / LPR;  // row groups a workgroup
+  const uint32_t rows = (uint32_t)p.B * p.NH * p.S;
+  const uint32_t r0 = (blockIdx.x * RPB + threadIdx.x / LPR) * R;
   const int d = 8 * (threadIdx.x % LPR);
   const bool in = d < p.D;
-  const bool row_in = r < (long long)p.B * p.NH * p.S;
-  float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (in && row_in) Ops<TX>::load8(static_cast<const TX*>(p.x) + (size_t)r * p.D + d, x);
-  normalise<LPR>(x, in, 1.0f / (float)p.D, p.eps);
-  if (!in || !row_in) return;
-  const int h = (int)((r / p.S) % p.NH);
-  const long long b = r / p.S / p.NH, t = r % p.S;
-  if (p.weight) {
-    float w[8];
-    Ops<float>::load8(p.weight + (size_t)h * p.D + d, w);
+  Raw8<TX> raw[R];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= w[e];
-  }
-  if (p.bias) {
-    float c[8];
-    Ops<float>::load8(p.bias + (size_t)h * p.D + d, c);
+  for (int j = 0; j < R; ++j) raw[j].load(static_cast<const TX*>(p.x) + (size_t)(r0 + j) * p.D + d, in && r0 + j < rows);
+  uint32_t bh = r0 / p.S, t = r0 - bh * p.S, h = bh % p.NH;
+  float w[8], c[8];
+  auto affine = [&] {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += c[e];
+    for (int e = 0; e < 8; ++e) {
+      w[e] = 1.0f;
+      c[e] = 0.0f;
+    }
+    if (in && p.weight) Ops<float>::load8(p.weight + (size_t)h * p.D + d, w);
+    if (in && p.bias) Ops<float>::load8(p.bias + (size_t)h * p.D + d, c);
+  };
+  affine();
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    float x[8];
+    raw[j].floats(x);
+    normalise<LPR>(x, in, 1.0f / (float)p.D, p.eps);
+    if (in && r0 + j < rows) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * w[e] + c[e];
+      store8f(static_cast<TY*>(p.y) + ((size_t)(bh / p.NH * p.S + t) * p.NH + h) * p.D + d, x);
+    }
+    if (j + 1 < R && ++t == (uint32_t)p.S) {
+      t = 0;
+      h = ++bh % p.NH;
+      affine();
+    }
   }
-  store8f(static_cast<TY*>(p.y) + (size_t)((b * p.S + t) * p.NH + h) * p.D + d, x);
 }
 
 template <typename TX, typename TY, int LPR>
@@ -108,18 +153,28 @@ __global__ __launch_bounds__(kThreads) void head_norm_back_kernel(const HeadNorm
     dw[e] = dc[e] = 0.0f;
   }
   if (in && p.weight) Ops<float>::load8(p.weight + (size_t)h * p.D + d, w);
-  const long long rows = (long long)p.B * p.S;
-  // the same trip count for every lane: the sums of a row run over lanes
-  for (long long i0 = (long long)blk * RPB; i0 < rows; i0 += (long long)p.blocks * RPB) {
-    const long long i = i0 + g;
+  const uint32_t rows = (uint32_t)p.B * p.S, step = (uint32_t)p.blocks * RPB;
+  auto offset = [&](uint32_t i) {
+    const uint32_t b = i / p.S, t = i - b * p.S;
+    return ((size_t)(b * p.NH + h) * p.S + t) * p.D + d;
+  };
+  Raw8<TX> rx;
+  Raw8<TY> ry;
+  auto fetch = [&](uint32_t i) {
     const bool ok = in && i < rows;
-    const long long b = i / p.S, t = i % p.S;
-    float n[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, dy[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    const size_t ox = (size_t)((b * p.NH + h) * p.S + t) * p.D + d;
-    if (ok) {
-      Ops<TX>::load8(static_cast<const TX*>(p.x) + ox, n);
-      Ops<TY>::load8(static_cast<const TY*>(p.dy) + (size_t)(i * p.NH + h) * p.D + d, dy);
-    }
+    rx.load(static_cast<const TX*>(p.x) + (ok ? offset(i) : 0), ok);
+    ry.load(static_cast<const TY*>(p.dy) + ((size_t)i * p.NH + h) * p.D + d, ok);
+  };
+  if (rows) fetch(blk * RPB + g);
+  // the same trip count for every lane: the sums of a row run over lanes; the
+  // next row's loads are on their way while this one is worked on
+  for (uint32_t i0 = blk * RPB; i0 < rows; i0 += step) {
+    const uint32_t i = i0 + g;
+    const bool ok = in && i < rows;
+    float n[8], dy[8];
+    rx.floats(n);
+    ry.floats(dy);
+    if (i0 + step < rows) fetch(i + step);
     const float rstd = normalise<LPR>(n, in, inv_d, p.eps);
     float sg = 0.0f, sgn = 0.0f, gw[8];
 #pragma unroll
@@ -138,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void head_norm_back_kernel(const HeadNorm
         dw[e] += dy[e] * n[e];
         dc[e] += dy[e];
       }
-      store8f(static_cast<TX*>(p.dx) + ox, dx);
+      store8f(static_cast<TX*>(p.dx) + offset(i), dx);
     }
   }
   if (!p.partial) return;
@@ -182,6 +237,7 @@ __global__ __launch_bounds__(kSumThreads) void head_norm_sum_kernel(const HeadNo
   if (out) out[h * p.D + d] = s;
 }
 
+constexpr long long kManyGroups = 2048;
 template <typename TX, typename TY, int LPR>
 hipError_t launch_rows(const HeadNormParams& p, bool back, hipStream_t stream) {
   const long long rpb = kThreads / LPR;
@@ -190,8 +246,12 @@ hipError_t launch_rows(const HeadNormParams& p, bool back, hipStream_t stream) {
                        0, stream, p);
   } else {
     const long long rows = (long long)p.B * p.NH * p.S;
-    hipLaunchKernelGGL((head_norm_kernel<TX, TY, LPR>), dim3((unsigned)((rows + rpb - 1) / rpb)), dim3(kThreads), 0,
-                       stream, p);
+    if (rows >= 4 * rpb * kManyGroups)
+      hipLaunchKernelGGL((head_norm_kernel<TX, TY, LPR, 4>), dim3((unsigned)((rows + 4 * rpb - 1) / (4 * rpb))),
+                         dim3(kThreads), 0, stream, p);
+    else
+      hipLaunchKernelGGL((head_norm_kernel<TX, TY, LPR, 1>), dim3((unsigned)((rows + rpb - 1) / rpb)), dim3(kThreads),
+                         0, stream, p);
   }
   return hipGetLastError();
 }
