@@ -36,10 +36,13 @@ template <typename TIn, typename TH, int DK>
 struct GradLds {
   static constexpr int L = DeltaIn<TIn>::kChunk, NP = DeltaIn<TIn>::kParts, NH = DeltaIn<TH>::kParts;
   static constexpr int NB = NP == 1 ? 2 : 3;  // parts of the terms of dK alone, which is stored as TIn
-  // row tiles of the states a wave, waves, and buffers of a step.  At 256 rows
-  // a workgroup fills a CU's registers; smaller heads leave room for two
-  // workgroups, which hide each other's waits better than a second buffer.
-  static constexpr int KPW = DK == 64 ? 1 : 2, NW = DK / (16 * KPW), BUFS = DK == 256 ? 2 : 1;
+  // Row tiles of the states a wave, waves, and buffers of a step.  At 256 rows
+  // a workgroup of eight waves fills a CU's registers, and a second buffer
+  // takes a barrier out of the step.  Smaller heads leave room for two
+  // workgroups, which hide each other's waits better than a second buffer (64
+  // heads of 128 x 128, 2048 tokens: 164 us against 205 with one workgroup and
+  // two buffers, and 203 with two row tiles a wave and so half the waves).
+  static constexpr int KPW = DK == 256 ? 2 : 1, NW = DK / (16 * KPW), BUFS = DK == 256 ? 2 : 1;
   static constexpr int kLdT = 40, kPlaneT = L * kLdT;  // 32 value columns
   // planes of a step: dH, U, dV, w U, -e dV
   static constexpr int kU = NH * kPlaneT, kR = kU + 3 * kPlaneT, kUw = kR + NB * kPlaneT, kRe = kUw + NB * kPlaneT;
@@ -69,19 +72,18 @@ struct StateRows {
   }
 };
 
-// Four values of a row in memory, zeros where `in` is false.
+// Four values of a row: element `off` of a resource over the chunk's rows
+// (zeros behind them), from column v0 on.
 template <typename T>
 struct Quad {
   words4_t x;
-  __device__ __forceinline__ void load(const T* p, bool in) {
-    x = (words4_t){0u, 0u, 0u, 0u};
-    if (!in) return;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int off, int v0) {
     if constexpr (sizeof(T) == 2) {
-      const words2_t w = *reinterpret_cast<const words2_t*>(p);
-      x[0] = w[0];
-      x[1] = w[1];
+      const v2i32_t w = __builtin_amdgcn_raw_buffer_load_b64(r, 2 * off, 2 * v0, 0);
+      x[0] = (uint32_t)w[0];
+      x[1] = (uint32_t)w[1];
     } else {
-      x = *reinterpret_cast<const words4_t*>(p);
+      x = __builtin_bit_cast(words4_t, __builtin_amdgcn_raw_buffer_load_b128(r, 4 * off, 4 * v0, 0));
     }
   }
   __device__ __forceinline__ float4_t values() const {
@@ -102,7 +104,7 @@ __device__ __forceinline__ void store_quads(uint16_t* p, int plane, const float4
 }
 
 template <typename TIn, typename TH, int DK>
-__global__ __launch_bounds__((64 * GradLds<TIn, TH, DK>::NW)) __attribute__((amdgpu_waves_per_eu(2))) void
+__global__ __launch_bounds__((64 * GradLds<TIn, TH, DK>::NW)) __attribute__((amdgpu_waves_per_eu(2 * GradLds<TIn, TH, DK>::NW / (DK == 256 ? 8 : 4)))) void
 delta_grads_kernel(const DeltaParams p) {
   typedef GradLds<TIn, TH, DK> W;
   constexpr int L = W::L, NP = W::NP, NH = W::NH, NB = W::NB, KPW = W::KPW, NW = W::NW, THREADS = 64 * NW;
@@ -135,23 +137,29 @@ delta_grads_kernel(const DeltaParams p) {
   // this wave's rows of the states, this thread's quads of the rest
   const uint32_t rows_bytes = 16u * KPW * (uint32_t)DV * 4u;
   const size_t first = (at * DK + 16 * KPW * __builtin_amdgcn_readfirstlane(wave)) * DV;
-  const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.C_states + first, rows_bytes);
-  const __amdgpu_buffer_rsrc_t rg = make_rsrc(p.G_states + first, rows_bytes);
+  const __amdgpu_buffer_rsrc_t r_c = make_rsrc(p.C_states + first, rows_bytes);
+  const __amdgpu_buffer_rsrc_t r_g = make_rsrc(p.G_states + first, rows_bytes);
   const int state_off = 4 * (row * DV + 8 * grp), row16 = 64 * DV;
   StateRows<KPW> xc, xg;
   Quad<float> qu[ROWS], qr[ROWS];
   Quad<TH> qh[ROWS];
   Quad<TIn> qv[ROWS];
+  const uint32_t in_seq = (uint32_t)DV * min(L, p.S - t0);
+  const __amdgpu_buffer_rsrc_t r_u = make_rsrc(p.U + at * L * DV, 4u * L * DV);
+  const __amdgpu_buffer_rsrc_t r_dv = make_rsrc(p.R + at * L * DV, 4u * L * DV);
+  const size_t seq0 = ((size_t)bh * p.S + t0) * DV;
+  const __amdgpu_buffer_rsrc_t r_dh = make_rsrc(static_cast<const TH*>(p.dH) + seq0, (uint32_t)sizeof(TH) * in_seq);
+  const __amdgpu_buffer_rsrc_t r_v = make_rsrc(static_cast<const TIn*>(p.V) + seq0, (uint32_t)sizeof(TIn) * in_seq);
+  // rows behind the chunk (float32 inputs: there are more threads than quads)
+  // read as zeros and are not staged
   auto fetch = [&](int v0) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int quad = tid + i * THREADS, t = quad >> 3, cc = v0 + 4 * (quad & 7);
-      const bool in = quad < QUADS, in_seq = in && t0 + t < p.S;
-      const size_t o = (at * L + t) * DV + cc, g = ((size_t)bh * p.S + t0 + t) * DV + cc;
-      qu[i].load(p.U + o, in);
-      qr[i].load(p.R + o, in);
-      qh[i].load(static_cast<const TH*>(p.dH) + g, in_seq);
-      qv[i].load(static_cast<const TIn*>(p.V) + g, in_seq);
+      const int quad = tid + i * THREADS, off = (quad >> 3) * DV + 4 * (quad & 7);
+      qu[i].load(r_u, off, v0);
+      qr[i].load(r_dv, off, v0);
+      qh[i].load(r_dh, off, v0);
+      qv[i].load(r_v, off, v0);
     }
   };
   auto stage = [&](uint16_t* s) {
@@ -183,8 +191,8 @@ delta_grads_kernel(const DeltaParams p) {
     qw[i] = p.w[at * L + t];
   }
   fetch(0);
-  xc.load(rc, state_off, row16, 0);
-  xg.load(rg, state_off, row16, 0);
+  xc.load(r_c, state_off, row16, 0);
+  xg.load(r_g, state_off, row16, 0);
   stage(s_K);
   if (DV > 32) fetch(32);
 
@@ -205,8 +213,8 @@ delta_grads_kernel(const DeltaParams p) {
       gp[i] = split_parts<NB>(b);
     }
     if (v0 + 32 < DV) {
-      xc.load(rc, state_off, row16, v0 + 32);
-      xg.load(rg, state_off, row16, v0 + 32);
+      xc.load(r_c, state_off, row16, v0 + 32);
+      xg.load(r_g, state_off, row16, v0 + 32);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
