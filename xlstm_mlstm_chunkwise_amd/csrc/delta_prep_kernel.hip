@@ -35,7 +35,7 @@ __global__ __launch_bounds__(4 * DeltaIn<TIn>::kChunk) void delta_prep_kernel(co
   constexpr int W = DK < 128 ? DK : 128;  // columns of K and Q at a time: four workgroups fit a CU
   constexpr int kTiles = 2 * NP * L * W * 2, kSquares = 2 * L * LDA * 4;
   __shared__ double s_b[L];
-  __shared__ float s_beta[L];
+  __shared__ __align__(16) float s_beta[L];
   __shared__ uint4 smem[(kTiles > kSquares ? kTiles : kSquares) / 16];
   uint16_t* s_K = reinterpret_cast<uint16_t*>(smem);  // first K and Q,
   uint16_t* s_Q = s_K + NP * L * W;
@@ -169,12 +169,25 @@ __global__ __launch_bounds__(4 * DeltaIn<TIn>::kChunk) void delta_prep_kernel(co
         ts = up ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : (f - 2) & 1);
       }
       const int a = 16 * rt + (l & 15);
+      // read whole, then cut at the diagonal: what is above it is in range, but
+      // nobody has written it
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int b = 32 * ts + o + (e & 3) + 16 * (e >> 2);
-        const int t = up ? b : a, col = up ? a : b;
-        x[e] = col <= t ? M[t * LDA + col] * (beta ? s_beta[col] : 1.0f) : 0.0f;
+      for (int half = 0; half < 2; ++half) {
+        const int b = 32 * ts + o + 16 * half;
+        float4_t m, scale = {1.0f, 1.0f, 1.0f, 1.0f};
+        if (up) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m[e] = M[(b + e) * LDA + a];
+        } else {
+          m = *reinterpret_cast<const float4_t*>(M + a * LDA + b);
+          if (beta) scale = *reinterpret_cast<const float4_t*>(s_beta + b);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool low = up ? a <= b + e : b + e <= a;
+          x[4 * half + e] = low ? m[e] * (beta ? up ? s_beta[a] : scale[e] : 1.0f) : 0.0f;
+        }
       }
       const Parts<3> y = planes == 3 ? split_parts<3>(x) : widen_parts(split_parts<2>(x));
       for (int n = 0; n < planes; ++n)
