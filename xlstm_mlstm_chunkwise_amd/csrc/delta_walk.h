@@ -51,14 +51,15 @@ struct RawTiles {
 
 // Every row is in range: the row offset may be a scalar, which the range
 // check leaves out.
+__device__ __forceinline__ void store_rows(const Slice<float>& s, int rt, const float4_t& x) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[r]), s.rsrc, s.lane_off, (16 * rt + r) * s.row_bytes, 0);
+}
 template <int N>
 __device__ __forceinline__ void store_whole(const Slice<float>& s, const float4_t (&x)[N]) {
 #pragma unroll
-  for (int rt = 0; rt < N; ++rt)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[rt][r]), s.rsrc, s.lane_off,
-                                            (16 * rt + r) * s.row_bytes, 0);
+  for (int rt = 0; rt < N; ++rt) store_rows(s, rt, x[rt]);
 }
 template <int N>
 __device__ __forceinline__ void load_whole(const Slice<float>& s, float4_t (&x)[N]) {

@@ -114,9 +114,16 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     v.load(Slice<TIn>(V + (size_t)t0 * p.DV, p.DV, rows, io_off));
     __builtin_amdgcn_sched_barrier(0);  // all loads are on their way
 
-    if constexpr (!FWD) {
-      store_whole(Slice<float>(p.C_states + at * DK * p.DV, p.DV, DK, io_off), C);
-    }
+    // The state entering a chunk leaves in two halves: the even tiles as soon
+    // as the chunk before has finished them, the odd ones before they are
+    // scaled.  All at once they fill the store queue, and the waves wait.
+    const Slice<float> keep(FWD ? nullptr : p.C_states + at * DK * p.DV, p.DV, FWD ? 0 : DK, io_off);
+    const Slice<float> keep_next(FWD ? nullptr : p.C_states + (at + 1) * DK * p.DV, p.DV, FWD || c + 1 == p.Nc ? 0 : DK,
+                                 io_off);
+    if constexpr (!FWD)
+      if (c == 0)
+#pragma unroll
+        for (int k = 0; k < KT; k += 2) store_rows(keep, k, C[k]);
 
     // K C and Q C: a step is one 32-row block of the state against K's rows,
     // the next one against Q's.  A block that has become operand parts is
@@ -146,6 +153,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) f[rt] = next[rt];
         }
+        if constexpr (!FWD) store_rows(keep, 2 * ks + 1, C[2 * ks + 1]);
         C[2 * ks] *= g;
         C[2 * ks + 1] *= g;
         if (more) {
@@ -217,11 +225,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
       tile_cols_times<NP, DK, 3>(s_K, W::kPlane, col_seed, ts, wp[ts], C, [&](int i) {
         const int rt = ts * (DK / 32) + i;
         if (FWD && rt < RT) store_tile(out, rt, qc[rt], p.scale, lane);
+        if (!FWD && ts == TS - 1 && i > 0) store_rows(keep_next, 2 * i - 2, C[2 * i - 2]);
         if (DB && ts == TS - 1)
 #pragma unroll
           for (int part = 0; part < 4; ++part)
             if (i == (part < DK / 32 ? part : DK / 32 - 1)) store(buf ^ 1, part);
       });
+    if constexpr (!FWD) store_rows(keep_next, KT - 2, C[KT - 2]);
   }
 
   if (p.C_out) store_whole(Slice<float>(p.C_out + (size_t)bh * DK * p.DV, p.DV, DK, io_off), C);
@@ -296,7 +306,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     load_whole(Slice<float>(p.U + at * L * p.DV, p.DV, L, io_off), u);
     raw.load(Slice<TH>(dH + (size_t)t0 * p.DV, p.DV, rows, io_off));
     __builtin_amdgcn_sched_barrier(0);  // all loads are on their way
-    store_whole(Slice<float>(p.G_states + at * DK * p.DV, p.DV, DK, io_off), G);
+    // in two halves, as the forward states
+    const Slice<float> keep_g(p.G_states + at * DK * p.DV, p.DV, DK, io_off);
+    const Slice<float> keep_next(p.G_states + (at - (c > 0)) * DK * p.DV, p.DV, c > 0 ? DK : 0, io_off);
+    if (c == p.Nc - 1)
+#pragma unroll
+      for (int k = 0; k < KT; k += 2) store_rows(keep_g, k, G[k]);
 
     // w K G, and its product with u; blocks of G are scaled by g on the way
     const float g = s_e[L - 1];
@@ -313,6 +328,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
+        store_rows(keep_g, 2 * ks + 1, G[2 * ks + 1]);
         G[2 * ks] *= g;
         G[2 * ks + 1] *= g;
         if (ks + 1 < DK / 32) {
@@ -373,10 +389,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
         const int rt = ts * (DK / 32) + i;
         if (rt < RT) {
           store_tile(out, rt, dv[rt], 1.0f, lane);
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dv[rt][r]), keep.rsrc, keep.lane_off,
-                                                  (16 * rt + r) * keep.row_bytes, 0);
+          store_rows(keep, rt, dv[rt]);
         }
         if (i == DK / 32 - 1) {
 #pragma unroll
@@ -385,7 +398,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
         }
       });
 #pragma unroll
-    for (int ts = 0; ts < TS; ++ts) tile_cols_times<NP, DK, 2>(s_K, W::kPlane, col_seed, ts, xp[ts], G);
+    for (int ts = 0; ts < TS; ++ts)
+      tile_cols_times<NP, DK, 2>(s_K, W::kPlane, col_seed, ts, xp[ts], G, [&](int i) {
+        if (ts == TS - 1 && i > 0) store_rows(keep_next, 2 * i - 2, G[2 * i - 2]);
+      });
+    store_rows(keep_next, KT - 2, G[KT - 2]);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) anchor += __shfl_xor(anchor, o, 64);
     if (lane == 0) p.anchor[at * (p.DV / 16) + slice * NW + wave] = anchor;
