@@ -543,7 +543,12 @@ int mlstm_bw_grads(const mlstm_fw_desc_t* desc,
  * those of the conventions at the top of this file.  Gates may be infinite:
  * f_t = -inf clears the memory before step t exactly (a document's end),
  * f_t = +inf keeps all of it, i_t = -inf writes nothing, i_t = +inf has
- * b_t = 1.  Other non-finite inputs spread as NaN.
+ * b_t = 1.  Other non-finite inputs (Q, K, V, dH, a NaN gate) give NaN, and
+ * not only in their own row: in all rows of the chunk they lie in (64 tokens,
+ * 32 for float32 inputs; a token before them included) and in every chunk
+ * that the state reaches from there, also past a forget gate of -inf.  Rows
+ * of padding therefore have to be finite (zeros with i_t = -inf write
+ * nothing), and in the backward pass their dH too.
  *
  * Arithmetic: every operand computed in float32 (the state, U, the inverse
  * within a chunk) enters the bf16 matrix cores in three parts of eight bits,
@@ -566,10 +571,12 @@ typedef struct {
 int mlstm_delta_validate(const mlstm_delta_desc_t* desc);
 
 /* Bytes of device workspace of mlstm_delta_fw and mlstm_delta_bw; 0 for an
- * invalid descriptor.  Forward: two L x L float32 matrices and three decays a
- * row for every chunk of L rows (64; 32 for float32 inputs).  Backward: also
- * the state entering and the state gradient behind every chunk (DHQK x DHV
- * float32 each), and U and dV in float32. */
+ * invalid descriptor.  Forward: two triangles as bf16 operand parts (18 KiB
+ * each for a chunk of 64 rows, 6 KiB for one of 32, float32 inputs) and, a
+ * row, a double and two floats of decays.  Backward: also the transpose of one
+ * triangle, the state entering and the state gradient behind every chunk (DHQK
+ * x DHV float32 each), U and dV in float32, and a float for every sixteen
+ * value columns of a chunk. */
 size_t mlstm_delta_fw_workspace_bytes(const mlstm_delta_desc_t* desc);
 size_t mlstm_delta_bw_workspace_bytes(const mlstm_delta_desc_t* desc);
 

@@ -813,7 +813,9 @@ def mlstm_delta_fw(q, k, v, i_pre, f_pre, C0=None, *, h_dtype=None, qk_scale: Op
     float32; C0 (B, NH, DHQK, DHV) float32 or None (zero state).  Returns
     (H, C); C is None when return_final_state is False.  H is float32 unless
     h_dtype or out says otherwise.  Keys are taken as they are: with
-    sigmoid(i_pre) |k|^2 < 2 the state stays bounded.
+    sigmoid(i_pre) |k|^2 < 2 the state stays bounded.  Rows of padding have to
+    be finite (a NaN reaches its whole chunk and all later ones); zeros with
+    i_pre = -inf write nothing.
     """
     torch = _torch()
     B, NH, S, DK, DV = _delta_inputs(q, k, v, i_pre, f_pre, C0)

@@ -22,6 +22,15 @@
 // T_ij = -T_ii sum_{j <= m < i} A_im T_mj, on the float32 matrix cores.  It is
 // the recurrence itself in another order, without the powers of A that would
 // grow for keys that repeat.
+//
+// 64 heads of 128 x 128 at 2048 tokens (2048 chunks): 40 us, 43 us with T^T;
+// 64 heads of 256 x 512 at 8192 tokens: 170 and 197 us, 0.82 and 0.97 GB moved.
+// It is bound by its chain of dependent steps (the waves wait 59 % of their
+// time, the vector units are busy half of it): a row of scans, the inverse's four
+// diagonal blocks and three rounds of products below them.  Four workgroups a
+// CU hide part of that; whole rows of K and Q in LDS leave room for two (250
+// against 181 us at 256 columns), and forward substitution over all 64 rows
+// instead of sixteen took 268 us.
 #include "delta_common.h"
 #include "kernels.h"
 

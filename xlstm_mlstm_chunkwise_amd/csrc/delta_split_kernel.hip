@@ -17,6 +17,14 @@
 // ahead in registers.  The loads go out in three lots between the phases: a
 // chunk is 94 KB, which a CU takes in no faster than 64 bytes a cycle, and a
 // wave that issues all its loads at once computes nothing meanwhile.
+//
+// A chunk's chain of dependent steps bounds it, not memory (with all loads
+// answered by the caches it is no faster): 8 heads of 256 x 512 at 65536
+// tokens, 1024 chunks one after another, take 3.1 ms, 3.0 us a chunk, of which
+// the matrix cores are busy a fifth; the column walk takes 6.8 ms there.  64
+// heads of 128 x 128 at 2048 tokens: 121 us forward, 122 with the states, 195
+// backward.  Two row tiles a wave instead of one cost 80 us against 68 for 15
+// heads of 64 x 192 at 1777 tokens.
 #include "delta_walk.h"
 
 namespace mlstm {

@@ -8,7 +8,9 @@
 // or 64 columns): thread (row group, column quad) holds 16-byte pieces of
 // every 16th row, all loads issued before anything waits on them, with
 // non-temporal accesses as in the step of the plain cell (a model's other
-// layers pass through the caches between two steps of one layer).
+// layers pass through the caches between two steps of one layer).  64 heads
+// of 256 x 512: 11.6 us for 67.5 MB (5.8 TB/s); with 128 columns a workgroup
+// 12.1 us.
 #include "device_common.h"
 #include "kernels.h"
 

@@ -10,7 +10,21 @@
 // The accumulator tiles of C, of V - e K C and of U feed straight back as
 // the right operand of the next product: the slot order of two accumulator
 // tiles is matched by how the left operands are read from LDS.  The next
-// chunk's K, Q, T and P are loaded into registers while this one computes.
+// chunk's K, Q, T and P are loaded into registers while this one computes and,
+// where two buffers fit, stored to LDS under its last products; the backward
+// walk, whose registers are full, stores them between two barriers.
+//
+// Bounds, at 64 heads of 256 x 512, 8192 tokens (128 chunks one after another
+// on every CU):
+// - the forward walk, 1.28-1.38 ms, by the matrix and vector instructions of
+//   its waves together: the matrix cores are busy 50 % of the time at the 2.0
+//   GHz that the load leaves, and of two conversions a matrix instruction the
+//   third no longer hides.  Without the products with the state it would be
+//   1.01 ms, without those of K^T 1.04, without the staging 1.29 (of 1.50).
+//   Its 1.65 GB would take 0.32 ms.
+// - the walk that keeps the states, 1.33 ms, and the backward walk, 2.48 ms,
+//   also by the 4.3 GB of states each: written all at once at the start of a
+//   chunk they took 1.65 and 2.55 ms, the waves waiting for the store queue.
 #include "delta_walk.h"
 
 namespace mlstm {
@@ -429,7 +443,11 @@ hipError_t launch_nw(const DeltaParams& p, DeltaWalk what, hipStream_t stream) {
 }
 
 // Waves a workgroup, sixteen columns each: eight where that still leaves a
-// workgroup for every CU, since they share the staging of K, Q, T and P.
+// workgroup for every CU (256), since they share the staging of K, Q, T and P.
+// Forward and backward pass in us at 2048 tokens, 64 heads of 128 x 512 (256
+// workgroups of eight): 228 and 1240, with four waves 316 and 1418; 256 heads
+// of 128 x 128: 333 and 1549, with four 434 and 1735.  Below that eight waves
+// would leave CUs idle.
 template <typename TIn, typename TH, int DK>
 hipError_t launch_dk(const DeltaParams& p, DeltaWalk what, hipStream_t stream) {
   if (p.DV % 128 == 0 && (long long)p.BH * (p.DV / 128) >= 256) return launch_nw<TIn, TH, DK, 8>(p, what, stream);
@@ -450,6 +468,13 @@ hipError_t launch_types(const DeltaParams& p, DeltaWalk what, hipStream_t stream
 
 hipError_t launch_delta_walk(const DeltaParams& p, DeltaWalk what, hipStream_t stream) {
   if (p.DV <= 0 || p.DV % 64 != 0) return hipErrorInvalidValue;
+  // Four-wave workgroups for every CU, or the form with the state's rows split
+  // over the waves.  Forward and backward pass in us at 2048 tokens: 64 heads
+  // of 128 x 128 (128 such workgroups) 177 and 601, split 148 and 569; 16 of
+  // 256 x 512 (128) 219 and 735, split 209 and 667; 64 of 128 x 256 (256) 179
+  // and 775, split 254 and 976; 32 of 256 x 512 (256) 240 and 1037, split 404
+  // and 1345; float32, 1024 tokens, 64 of 128 x 256 (256) 160 and 588, split
+  // 204 and 702.
   if ((long long)p.BH * (p.DV / 64) < 256) return launch_delta_split(p, what, stream);
   if (p.qkv_bf16)
     return p.h_bf16 ? launch_types<bf16_t, bf16_t>(p, what, stream) : launch_types<bf16_t, float>(p, what, stream);
