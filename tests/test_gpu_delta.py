@@ -379,3 +379,172 @@ def test_more_columns_a_workgroup(mt):
         r = delta_grad(*_oracle_args(x), x["dH"], x["C0"])
         for n in ("dQ", "dK", "dV", "d_i", "d_f", "dC0"):
             _close(g[n], r[n], GATE if n == "d_f" else DK_BF16 if n == "dK" else F32, n)
+
+
+def test_two_streams_at_once(mt):
+    """Calls on two streams without a wait between them, each with its own
+    inputs: the bits of one after the other."""
+    sets = [_gpu(_draw(81 + j, 2, 2, 300, 128, 128, "bf16"), "bf16") for j in range(2)]
+    dH = [_dev(_draw(83 + j, 2, 2, 300, 128, 128, "bf16")["dH"], torch.bfloat16) for j in range(2)]
+
+    def work(j):
+        args, C0 = sets[j]
+        H, C = mt.mlstm_delta_fw(*args, C0)
+        g = mt.mlstm_delta_bw(*args, dH[j], C0, state_grads=True)
+        return [H, C, mt.head_norm_fw(H)] + [g[n] for n in sorted(g)]
+
+    want = [work(j) for j in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for j, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((j, work(j)))
+    torch.cuda.synchronize()
+    for j, out in got:
+        assert all(torch.equal(a, b) for a, b in zip(out, want[j]))
+
+
+def test_two_graphs_that_share_a_workspace(mt):
+    """Replayed one after the other, in any order, with eager calls on the same
+    workspace between them."""
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for j, (S, DK) in enumerate(((100, 64), (150, 128))):
+        x = _draw(91 + j, 1, 2, S, DK, 64, "bf16")
+        args, C0 = _gpu(x, "bf16")
+        dH = _dev(x["dH"], torch.bfloat16)
+
+        def work(args=args, C0=C0, dH=dH):
+            H, C = mt.mlstm_delta_fw(*args, C0, workspace=ws)
+            g = mt.mlstm_delta_bw(*args, dH, C0, workspace=ws)
+            return [H, C] + [g[n] for n in sorted(g)]
+
+        want = [o.clone() for o in work()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = work()
+        graphs.append((graph, out, want, work))
+    for j in (0, 1, 1, 0, 1, 0):
+        graph, out, want, _ = graphs[j]
+        for o in out:
+            o.zero_()
+        graph.replay()
+        eager = graphs[1 - j][3]()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert all(torch.equal(a, b) for a, b in zip(eager, graphs[1 - j][2]))
+
+
+@pytest.mark.parametrize("DV,B", [(64, 1), (512, 32)])
+def test_a_nan_leaves_other_heads_and_earlier_chunks(mt, DV, B):
+    """Both forms of the walk (few columns, many)."""
+    x = _draw(95, B, 2, 200, 64, DV, "bf16")
+    args, C0 = _gpu(x, "bf16")
+    H, C = mt.mlstm_delta_fw(*args, C0)
+    args[1][0, 0, 100, 5] = float("nan")
+    H2, C2 = mt.mlstm_delta_fw(*args, C0)
+    assert H2[0, 0, 100:].isnan().any() and C2[0, 0].isnan().any()
+    assert torch.equal(H2[0, 0, :64], H[0, 0, :64])
+    assert torch.equal(H2[0, 1], H[0, 1]) and torch.equal(H2[1:], H[1:]) and torch.equal(C2[0, 1], C[0, 1])
+
+
+def test_padding_of_zeros(mt):
+    """Rows of zeros with i = -inf behind a sequence, f anything: the state
+    decays by the forget gates only, the rows before are as without them, and
+    their gradients too."""
+    x = _draw(97, 2, 2, 90, 64, 128, "bf16")
+    args, C0 = _gpu(x, "bf16")
+    dH = _dev(x["dH"], torch.bfloat16)
+    pad = [torch.cat([a, torch.zeros_like(a[:, :, :50])], 2) for a in args]
+    pad[3][:, :, 90:] = float("-inf")
+    pad[4][:, :, 90:] = float("inf")
+    H, C = mt.mlstm_delta_fw(*args, C0)
+    H2, C2 = mt.mlstm_delta_fw(*pad, C0)
+    Hr, Cr = delta_fw(*_oracle_args(x), x["C0"])
+    _close(H2[:, :, :90], Hr, F32, "H")
+    _close(C2, Cr, F32, "C")
+    assert (H2[:, :, 90:] == 0).all()
+    dHp = torch.cat([dH, torch.ones_like(dH[:, :, :50])], 2)
+    g = mt.mlstm_delta_bw(*pad, dHp, C0, state_grads=True)
+    r = delta_grad(*_oracle_args(x), x["dH"], x["C0"])
+    for n in ("dQ", "dK", "dV", "d_i", "d_f", "dC0"):
+        rel = GATE if n == "d_f" else DK_BF16 if n == "dK" else F32
+        _close(g[n] if n == "dC0" else g[n][:, :, :90], r[n], rel, n)
+    assert (g["dV"][:, :, 90:] == 0).all() and (g["d_i"][:, :, 90:] == 0).all()
+
+
+def test_one_tensor_for_queries_and_keys(mt):
+    x = _draw(99, 1, 2, 70, 64, 64, "f32")
+    x["q"] = x["k"]
+    args, C0 = _gpu(x, "f32")
+    key = args[1].requires_grad_(True)
+    mt.mlstm_delta(key, key, *args[2:], C0).backward(_dev(x["dH"], torch.float32))
+    r = delta_grad(*_oracle_args(x), x["dH"], x["C0"])
+    _close(key.grad, r["dQ"] + r["dK"], F32, "dQ + dK", 2)
+
+
+def test_a_broadcast_gradient(mt):
+    x = _draw(101, 1, 2, 70, 64, 64, "bf16")
+    args, C0 = _gpu(x, "bf16")
+    leaves = [a.requires_grad_(True) for a in args]
+    H = mt.mlstm_delta(*leaves, C0)
+    H.sum().backward()
+    g = mt.mlstm_delta_bw(*[a.detach() for a in args], torch.ones_like(H), C0)
+    assert all(torch.equal(a.grad, g[n]) for a, n in zip(leaves, ("dQ", "dK", "dV", "d_i", "d_f")))
+
+
+def test_refused_with_tensors_on_the_gpu(mt):
+    x = _draw(103, 1, 2, 70, 64, 64, "bf16")
+    args, C0 = _gpu(x, "bf16")
+    dH = _dev(x["dH"], torch.bfloat16)
+    q, k, v, i, f = args
+    turned = q.transpose(2, 3).contiguous().transpose(2, 3)
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    for call in (lambda: mt.mlstm_delta_fw(turned, k, v, i, f), lambda: mt.mlstm_delta_fw(q, k[:, :, 1:], v, i, f),
+                 lambda: mt.mlstm_delta_fw(q, k, v.cpu(), i, f), lambda: mt.mlstm_delta_fw(q, k, v, i, f, C0[:, :1]),
+                 lambda: mt.mlstm_delta_fw(q, k, v, i, f, C0[:, :1].expand(1, 2, 64, 64)),
+                 lambda: mt.mlstm_delta_fw(q, k, v, i, f, workspace=small),
+                 lambda: mt.mlstm_delta_fw(q, k, v, i, f, workspace=small.cpu()),
+                 lambda: mt.mlstm_delta_bw(q, k, v, i, f, dH[:, :, :69]),
+                 lambda: mt.mlstm_delta_bw(q, k, v, i, f, dH, workspace=small),
+                 lambda: mt.head_norm_fw(turned), lambda: mt.head_norm_bw(q, q),
+                 lambda: mt.head_norm_fw(q, torch.ones(2, 32, device="cuda")),
+                 lambda: mt.head_norm_fw(q, torch.ones(2, 64))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: mt.mlstm_delta_fw(q, k.float(), v, i, f), lambda: mt.mlstm_delta_fw(q, k, v, i.bfloat16(), f),
+                 lambda: mt.mlstm_delta_fw(q, k, v, i, f, h_dtype=torch.float16),
+                 lambda: mt.head_norm_fw(q, torch.ones(2, 64, device="cuda", dtype=torch.bfloat16))):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    bad = torch.zeros(1, 1, 4, 96, device="cuda")
+    with pytest.raises(mt.MlstmError):
+        mt.mlstm_delta_fw(bad, bad, bad, bad[..., 0].contiguous(), bad[..., 0].contiguous())
+
+
+def test_offsets_beyond_32_bits(mt):
+    """Four million tokens of one head (Q, K over 2^31 bytes, the states 4.3
+    GB): behind a closed forget gate on a chunk's border the rows are those of
+    a short sequence, each side off by F32."""
+    t0 = 1 << 22
+    S = t0 + 77
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    q, k = (torch.empty(1, 1, S, 256, dtype=torch.bfloat16, device="cuda").normal_(0.0, 1 / 16, generator=gen)
+            for _ in range(2))
+    v, dH = (torch.empty(1, 1, S, 64, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
+    i = torch.empty(1, 1, S, device="cuda").normal_(generator=gen)
+    f = torch.full((1, 1, S), 3.0, device="cuda")
+    f[0, 0, t0] = float("-inf")
+    args = (q, k, v, i, f)
+    tail = [a[:, :, t0:].contiguous() for a in args]
+    H, C = mt.mlstm_delta_fw(*args)
+    Ht, Ct = mt.mlstm_delta_fw(*tail)
+    g = mt.mlstm_delta_bw(*args, dH)
+    gt = mt.mlstm_delta_bw(*tail, dH[:, :, t0:].contiguous())
+    for n, a, b in [("H", H[:, :, t0:], Ht), ("C", C, Ct)] + [(n, g[n][:, :, t0:], gt[n]) for n in g]:
+        rel = GATE if n == "d_f" else DK_BF16 if n == "dK" else F32
+        _close(a, b.double().cpu().numpy(), rel, n, 2)
+    assert torch.isfinite(H).all() and all(torch.isfinite(x).all() for x in g.values())

@@ -153,3 +153,38 @@ def test_behind_the_cell(mt):
     assert all(torch.equal(a, c) for a, c in zip(got, want)) and torch.equal(got[-1], dw)
     with pytest.raises(ValueError):
         mt.mlstm_chunkwise(*args, chunk_size=64, norm_bias=w)
+
+
+@pytest.mark.parametrize("B,NH,S,D,xk,yk", [(3, 5, 2185, 512, "bf16", "f32"), (1, 16411, 2, 512, "f32", "bf16"),
+                                            (4, 8209, 1, 448, "bf16", "bf16"), (1, 3, 87391, 64, "f32", "f32")])
+def test_rows_four_at_a_time(mt, B, NH, S, D, xk, yk):
+    """Enough rows for four of them a lane group, heads ending inside a group."""
+    x, dy, w, b = _draw(S + D, B, NH, S, D, xk, yk)
+    for wd, bd in ((w, b), (None, None)):
+        y = mt.head_norm_fw(_dev(x, xk), *(None if a is None else _dev(a) for a in (wd, bd)), y_dtype=TYPES[yk])
+        ref = head_norm_fw(x, wd, bd)
+        _close(y, ref, ROW * np.abs(ref).max(), "y")
+    dx = mt.head_norm_bw(_dev(x, xk), _dev(dy, yk), _dev(w), weight_grads=False)[0]
+    rx = head_norm_grad(x, dy, w)[0]
+    _close(dx, rx, ROW * np.abs(rx).max(), "dx")
+
+
+def test_offsets_beyond_32_bits(mt):
+    """The most rows that are taken, 2^26 - 1 of 64 values: 8.6 GB of x."""
+    S = (1 << 26) - 1
+    x = torch.zeros(1, 1, S, 64, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros(1, S, 1, 64, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x[:, :, -1001:].normal_(generator=gen)
+    dy[:, -1001:].normal_(generator=gen)
+    w, b = torch.full((1, 64), 1.5, device="cuda"), torch.full((1, 64), 0.25, device="cuda")
+    xt, dyt = x[:, :, -1001:].contiguous(), dy[:, -1001:].contiguous()
+    y = mt.head_norm_fw(x, w, b)
+    assert torch.equal(y[:, -1001:], mt.head_norm_fw(xt, w, b)) and (y[:, :-1001] == 0.25).all()
+    dx, dw, db = mt.head_norm_bw(x, dy, w)
+    rx, rw, rb = mt.head_norm_bw(xt, dyt, w)
+    assert torch.equal(dx[:, :, -1001:], rx) and (dx[:, :, :-1001] == 0).all()
+    # the same 1001 terms, in other runs: each sum rounds by at most 2^-24 of the sum of their sizes
+    for got, want, term in ((dw, rw, 8.0 * dyt.float().abs()), (db, rb, dyt.float().abs())):
+        limit = 2 * 1001 * 2.0 ** -24 * term.sum(1)[0].max()
+        assert ((got - want).abs() <= limit).all()
