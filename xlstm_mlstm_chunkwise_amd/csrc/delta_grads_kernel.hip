@@ -20,9 +20,9 @@
 // terms of dK add into one accumulator.  Every load is issued a step ahead:
 // without that the step took the latency of memory three times over.
 //
-// 64 heads of 256 x 512 at 8192 tokens: 2.70 ms for 12.4 GB (4.6 TB/s; a large
-// copy reaches 5.1), two thirds of them the states.  64 heads of 128 x 128 at
-// 2048 tokens: 164 us; 15 of 64 x 192 at 1777 tokens: 34 us.
+// 64 heads of 256 x 512 at 8192 tokens: 2.70-2.81 ms for 12.4 GB (4.5 TB/s; a
+// large copy reaches 5.1), two thirds of them the states.  64 heads of 128 x 128 at
+// 2048 tokens: 164-171 us; 15 of 64 x 192 at 1777 tokens: 34 us.
 #include "delta_common.h"
 #include "kernels.h"
 

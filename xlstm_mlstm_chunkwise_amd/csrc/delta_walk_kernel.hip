@@ -16,13 +16,13 @@
 //
 // Bounds, at 64 heads of 256 x 512, 8192 tokens (128 chunks one after another
 // on every CU):
-// - the forward walk, 1.28-1.38 ms, by the matrix and vector instructions of
+// - the forward walk, 1.28-1.41 ms, by the matrix and vector instructions of
 //   its waves together: the matrix cores are busy 50 % of the time at the 2.0
 //   GHz that the load leaves, and of two conversions a matrix instruction the
 //   third no longer hides.  Without the products with the state it would be
 //   1.01 ms, without those of K^T 1.04, without the staging 1.29 (of 1.50).
 //   Its 1.65 GB would take 0.32 ms.
-// - the walk that keeps the states, 1.33 ms, and the backward walk, 2.48 ms,
+// - the walk that keeps the states, 1.31 ms, and the backward walk, 2.45 ms,
 //   also by the 4.3 GB of states each: written all at once at the start of a
 //   chunk they took 1.65 and 2.55 ms, the waves waiting for the store queue.
 #include "delta_walk.h"
