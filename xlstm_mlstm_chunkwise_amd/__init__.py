@@ -750,12 +750,13 @@ def _call(where, dev, *args):
     """Run a C entry point on dev's current stream (appended as the last
     argument); raises MlstmError for a non-zero status."""
     torch = _torch()
-    fn = getattr(lib(), where)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    fn, index = getattr(lib(), where), dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(index):
+            st = fn(*args, stream)
     if st:
         raise MlstmError(st, where)
 
@@ -795,7 +796,8 @@ def _delta_inputs(q, k, v, i_pre, f_pre, C0):
     dev = q.device
     if not q.is_cuda:
         raise ValueError("Q must be a GPU tensor")
-    _check_on(dev, "Q", q, (B, NH, S, DK), q.dtype)
+    if not q.is_contiguous():
+        raise ValueError("Q must be contiguous")
     _check_on(dev, "K", k, (B, NH, S, DK), q.dtype)
     _check_on(dev, "V", v, (B, NH, S, DV), q.dtype)
     _check_on(dev, "i_pre", i_pre, (B, NH, S), torch.float32)
@@ -824,7 +826,7 @@ def mlstm_delta_fw(q, k, v, i_pre, f_pre, C0=None, *, h_dtype=None, qk_scale: Op
     _check_on(dev, "H", out, (B, NH, S, DV), h_dtype)
     desc, need, _ = _delta_plan("mlstm_delta_fw", B, NH, S, DK, DV, q.dtype, h_dtype, qk_scale)
     workspace, ws_bytes = _bytes_of(need, workspace, dev)
-    H = torch.empty((B, NH, S, DV), dtype=h_dtype, device=dev) if out is None else out
+    H = torch.empty_like(v, dtype=h_dtype) if out is None else out
     C = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev) if return_final_state else None
     _call("mlstm_delta_fw", dev, desc, _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C0),
           _ptr(H), _ptr(C), _ptr(workspace), ws_bytes)
@@ -870,7 +872,8 @@ def mlstm_delta_step(q, k, v, i_pre, f_pre, C=None, *, h_dtype=None, qk_scale: O
     B, NH, DK = q.shape
     DV = v.shape[-1]
     dev = q.device
-    _check_on(dev, "q", q, (B, NH, DK), q.dtype)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
     _check_on(dev, "k", k, (B, NH, DK), q.dtype)
     _check_on(dev, "v", v, (B, NH, DV), q.dtype)
     _check_on(dev, "i_pre", i_pre, (B, NH), torch.float32)
@@ -879,7 +882,7 @@ def mlstm_delta_step(q, k, v, i_pre, f_pre, C=None, *, h_dtype=None, qk_scale: O
     _check_on(dev, "C_out", C_out, (B, NH, DK, DV), torch.float32)
     h_dtype = h_dtype or torch.float32
     desc, _, _ = _delta_plan("mlstm_delta_step", B, NH, 1, DK, DV, q.dtype, h_dtype, qk_scale)
-    h = torch.empty((B, NH, DV), dtype=h_dtype, device=dev)
+    h = torch.empty_like(v, dtype=h_dtype)
     if C_out is None:
         C_out = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev)
     _call("mlstm_delta_step", dev, desc, _ptr(q), _ptr(k), _ptr(v), _ptr(i_pre), _ptr(f_pre), _ptr(C),
@@ -967,7 +970,8 @@ def _norm_input(x):
     _out_code(x.dtype, "x")
     if not x.is_cuda:
         raise ValueError("x must be a GPU tensor")
-    _check_on(x.device, "x", x, x.shape, x.dtype)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     return x.shape
 
 
@@ -983,9 +987,10 @@ def head_norm_fw(x, weight=None, bias=None, *, eps: float = 1e-6, y_dtype=None, 
     y_dtype = y_dtype or (x.dtype if out is None else out.dtype)
     _check_on(dev, "weight", weight, (NH, D), torch.float32)
     _check_on(dev, "bias", bias, (NH, D), torch.float32)
-    _check_on(dev, "y", out, (B, S, NH, D), y_dtype)
+    if out is not None:
+        _check_on(dev, "y", out, (B, S, NH, D), y_dtype)
     desc, _ = _norm_plan("mlstm_head_norm_fw", B, NH, S, D, x.dtype, y_dtype, eps)
-    y = torch.empty((B, S, NH, D), dtype=y_dtype, device=dev) if out is None else out
+    y = x.new_empty((B, S, NH, D), dtype=y_dtype) if out is None else out
     _call("mlstm_head_norm_fw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y))
     return y
 
@@ -1009,8 +1014,13 @@ def _norm_grads(x, dy, weight, eps, weight_grad, bias_grad, workspace=None):
     dev = x.device
     desc, need = _norm_plan("mlstm_head_norm_bw", B, NH, S, D, x.dtype, dy.dtype, eps)
     dx, ws_bytes = torch.empty_like(x), 0
-    dw = torch.empty((NH, D), dtype=torch.float32, device=dev) if weight_grad else None
-    db = torch.empty((NH, D), dtype=torch.float32, device=dev) if bias_grad else None
+
+    def row():
+        if weight is not None:
+            return torch.empty_like(weight)
+        return torch.empty((NH, D), dtype=torch.float32, device=dev)
+
+    dw, db = row() if weight_grad else None, row() if bias_grad else None
     if weight_grad or bias_grad:
         workspace, ws_bytes = _bytes_of(need, workspace, dev)
     _call("mlstm_head_norm_bw", dev, desc, _ptr(x), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
