@@ -548,3 +548,37 @@ def test_offsets_beyond_32_bits(mt):
         rel = GATE if n == "d_f" else DK_BF16 if n == "dK" else F32
         _close(a, b.double().cpu().numpy(), rel, n, 2)
     assert torch.isfinite(H).all() and all(torch.isfinite(x).all() for x in g.values())
+
+
+def test_a_captured_training_pass(mt):
+    """Forward, norm and gradients through autograd in one graph (no eager
+    graph of the leaves is alive while it is captured), replayed with new
+    inputs between eager passes."""
+    x = _draw(111, 1, 3, 90, 64, 128, "bf16")
+    args, C0 = _gpu(x, "bf16")
+    w = (torch.rand(3, 128, device="cuda") + 0.5).requires_grad_(True)
+    leaves = [a.requires_grad_(True) for a in args + [C0]] + [w]
+    dy = _dev(x["dH"].transpose(0, 2, 1, 3), torch.bfloat16)
+
+    def work():
+        y, C = mt.mlstm_delta(*leaves[:6], return_final_state=True, norm_weight=w)
+        return [y.detach(), C.detach()] + list(torch.autograd.grad([y, C], leaves, [dy, torch.ones_like(C)]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for seed in range(3):
+        fresh, C1 = _gpu(_draw(112 + seed, 1, 3, 90, 64, 128, "bf16"), "bf16")
+        with torch.no_grad():
+            for a, b in zip(leaves, fresh + [C1]):
+                a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, work()))

@@ -929,7 +929,9 @@ def mlstm_delta(q, k, v, i_pre, f_pre, C0=None, *, h_dtype=None, qk_scale: Optio
     mlstm_delta_fw, the backward mlstm_delta_bw (gradients for q, k, v, i_pre,
     f_pre and C0).  Returns H, or (H, C) with return_final_state; gradients
     flow in through both.  norm_weight (NH, DHV), with norm_bias or without:
-    head_norm(H) takes H's place, (B, S, NH, DHV) in q's dtype."""
+    head_norm(H) takes H's place, (B, S, NH, DHV) in q's dtype.  A pass may be
+    captured into a graph as long as no eager graph of the same leaves is
+    alive meanwhile."""
     out = _delta_function().apply(q, k, v, i_pre, f_pre, C0, h_dtype, qk_scale, return_final_state)
     H, C = out if return_final_state else (out, None)
     H = _normed(H, q, norm_weight, norm_bias, norm_eps)
