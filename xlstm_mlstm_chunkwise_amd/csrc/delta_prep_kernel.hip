@@ -66,7 +66,8 @@ __global__ __launch_bounds__(4 * DeltaIn<TIn>::kChunk) void delta_prep_kernel(co
   if (wave == 0) {
     const int t = t0 + lane;
     const bool in = lane < L && t < p.S;
-    double b = in ? (double)fmaxf(log_sigmoid(p.f_pre[(size_t)bh * p.S + t]), kMinLogDecay) : 0.0;
+    const float lf = in ? log_sigmoid(p.f_pre[(size_t)bh * p.S + t]) : 0.0f;
+    double b = (double)(lf < kMinLogDecay ? kMinLogDecay : lf);  // a NaN stays one; fmaxf would close the gate
     const float ip = in ? p.i_pre[(size_t)bh * p.S + t] : -INFINITY;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
