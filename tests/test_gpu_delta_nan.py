@@ -87,3 +87,48 @@ def test_forget_gate_step(mt):
     h2, C2 = mt.mlstm_delta_step(*one, C0)
     _others_keep_their_bits(h2, h)
     _others_keep_their_bits(C2, C)
+
+
+@pytest.mark.parametrize("B,NH", FORMS)
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [0, 100])
+def test_input_gate(mt, B, NH, kind, t):
+    """b_t also stands in token t's own dV = b dU."""
+    args, C0, dH = _draw(B, NH, kind)
+    H, C = mt.mlstm_delta_fw(*args, C0)
+    want = mt.mlstm_delta_bw(*args, dH, C0, state_grads=True)
+    args[3][0, 0, t] = float("nan")
+    H2, C2 = mt.mlstm_delta_fw(*args, C0)
+    start = t // CHUNK[kind] * CHUNK[kind]
+    assert H2[0, 0, t:].isnan().all() and C2[0, 0].isnan().all()
+    assert torch.equal(H2[0, 0, :start], H[0, 0, :start])
+    _others_keep_their_bits(H2, H)
+    _others_keep_their_bits(C2, C)
+    g = mt.mlstm_delta_bw(*args, dH, C0, state_grads=True)
+    for n, rows in (("dQ", slice(t, None)), ("dK", slice(None)), ("dV", slice(t + 1)), ("d_i", slice(None)),
+                    ("d_f", slice(None)), ("dC0", slice(None))):
+        assert g[n][0, 0, rows].isnan().all(), n
+        _others_keep_their_bits(g[n], want[n])
+
+
+@pytest.mark.parametrize("B,NH", FORMS)
+def test_first_forget_gate_without_a_state(mt, B, NH):
+    """It multiplies a state of zeros, and its gradient is zero, unless it is
+    NaN itself."""
+    args, _, dH = _draw(B, NH, "bf16")
+    assert (mt.mlstm_delta_bw(*args, dH)["d_f"][..., 0] == 0).all()
+    args[4][0, 0, 0] = float("nan")
+    d_f = mt.mlstm_delta_bw(*args, dH)["d_f"]
+    assert d_f[0, 0].isnan().all()
+    assert (d_f[0, 1:, 0] == 0).all() and (d_f[1:, :, 0] == 0).all()
+
+
+def test_input_gate_step(mt):
+    args, C0, _ = _draw(2, 2, "f32")
+    one = [a[:, :, 0].contiguous() for a in args]
+    h, C = mt.mlstm_delta_step(*one, C0)
+    one[3][0, 0] = float("nan")
+    h2, C2 = mt.mlstm_delta_step(*one, C0)
+    assert h2[0, 0].isnan().all() and C2[0, 0].isnan().all()
+    _others_keep_their_bits(h2, h)
+    _others_keep_their_bits(C2, C)

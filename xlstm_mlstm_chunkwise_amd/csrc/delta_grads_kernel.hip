@@ -393,11 +393,11 @@ delta_grads_kernel(const DeltaParams p) {
       const size_t o = (size_t)bh * p.S + t0 + t;
       const float f = p.f_pre[o], ip = p.i_pre[o];
       // a gate that passes nothing has no gradient: its e^ is zero in float32,
-      // or it is the first and there is no state to pass
-      const bool closed = expf(log_sigmoid(f)) == 0.0f || (t0 + t == 0 && !p.C0);
+      // or it is the first and there is no state to pass (a NaN passes NaN)
+      const bool closed = expf(log_sigmoid(f)) == 0.0f || (t0 + t == 0 && !p.C0 && f == f);
       p.d_f[o] = closed ? 0.0f : d / (1.0f + expf(f));
       const float beta = 1.0f / (1.0f + expf(-ip));
-      p.d_i[o] = beta > 0.0f ? s_dvu[t] / beta * (1.0f - beta) : 0.0f;
+      p.d_i[o] = beta == 0.0f ? 0.0f : s_dvu[t] / beta * (1.0f - beta);
     }
   }
 }
