@@ -775,11 +775,17 @@ def _bytes_of(need, workspace, dev):
     return workspace, size
 
 
+def _scale(qk_scale) -> float:
+    """qk_scale as it is now: a tensor may change in place after the call."""
+    return 0.0 if qk_scale is None else float(qk_scale)
+
+
 @functools.lru_cache(maxsize=256)
 def _delta_plan(where, B, NH, S, DK, DV, qkv_dtype, h_dtype, qk_scale):
-    """Descriptor (as an argument) and workspace sizes, forward and backward."""
+    """Descriptor (as an argument) and workspace sizes, forward and backward,
+    kept by value: qk_scale is a Python float (_scale)."""
     desc = make_delta_desc(B, NH, S, DK, DV, qkv_dtype=_out_code(qkv_dtype, "Q/K/V"),
-                           h_dtype=_out_code(h_dtype, "h_dtype"), qk_scale=0.0 if qk_scale is None else float(qk_scale))
+                           h_dtype=_out_code(h_dtype, "h_dtype"), qk_scale=qk_scale)
     st = delta_validate(desc)
     if st:
         raise MlstmError(st, where)
@@ -824,7 +830,7 @@ def mlstm_delta_fw(q, k, v, i_pre, f_pre, C0=None, *, h_dtype=None, qk_scale: Op
     dev = q.device
     h_dtype = h_dtype or (torch.float32 if out is None else out.dtype)
     _check_on(dev, "H", out, (B, NH, S, DV), h_dtype)
-    desc, need, _ = _delta_plan("mlstm_delta_fw", B, NH, S, DK, DV, q.dtype, h_dtype, qk_scale)
+    desc, need, _ = _delta_plan("mlstm_delta_fw", B, NH, S, DK, DV, q.dtype, h_dtype, _scale(qk_scale))
     workspace, ws_bytes = _bytes_of(need, workspace, dev)
     H = torch.empty_like(v, dtype=h_dtype) if out is None else out
     C = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev) if return_final_state else None
@@ -846,7 +852,7 @@ def mlstm_delta_bw(q, k, v, i_pre, f_pre, dH, C0=None, dC=None, *, qk_scale: Opt
     dev = q.device
     _check_on(dev, "dH", dH, (B, NH, S, DV), dH.dtype)
     _check_on(dev, "dC", dC, (B, NH, DK, DV), torch.float32)
-    desc, _, need = _delta_plan("mlstm_delta_bw", B, NH, S, DK, DV, q.dtype, dH.dtype, qk_scale)
+    desc, _, need = _delta_plan("mlstm_delta_bw", B, NH, S, DK, DV, q.dtype, dH.dtype, _scale(qk_scale))
     workspace, ws_bytes = _bytes_of(need, workspace, dev)
     g = dict(dQ=torch.empty_like(q), dK=torch.empty_like(k), dV=torch.empty_like(v), d_i=torch.empty_like(i_pre),
              d_f=torch.empty_like(f_pre))
@@ -881,7 +887,7 @@ def mlstm_delta_step(q, k, v, i_pre, f_pre, C=None, *, h_dtype=None, qk_scale: O
     _check_on(dev, "C", C, (B, NH, DK, DV), torch.float32)
     _check_on(dev, "C_out", C_out, (B, NH, DK, DV), torch.float32)
     h_dtype = h_dtype or torch.float32
-    desc, _, _ = _delta_plan("mlstm_delta_step", B, NH, 1, DK, DV, q.dtype, h_dtype, qk_scale)
+    desc, _, _ = _delta_plan("mlstm_delta_step", B, NH, 1, DK, DV, q.dtype, h_dtype, _scale(qk_scale))
     h = torch.empty_like(v, dtype=h_dtype)
     if C_out is None:
         C_out = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev)
@@ -932,7 +938,7 @@ def mlstm_delta(q, k, v, i_pre, f_pre, C0=None, *, h_dtype=None, qk_scale: Optio
     head_norm(H) takes H's place, (B, S, NH, DHV) in q's dtype.  A pass may be
     captured into a graph as long as no eager graph of the same leaves is
     alive meanwhile."""
-    out = _delta_function().apply(q, k, v, i_pre, f_pre, C0, h_dtype, qk_scale, return_final_state)
+    out = _delta_function().apply(q, k, v, i_pre, f_pre, C0, h_dtype, _scale(qk_scale), return_final_state)
     H, C = out if return_final_state else (out, None)
     H = _normed(H, q, norm_weight, norm_bias, norm_eps)
     return (H, C) if return_final_state else H
@@ -957,9 +963,10 @@ def head_norm_bw_workspace_bytes(desc: HeadNormDesc) -> int:
 
 @functools.lru_cache(maxsize=256)
 def _norm_plan(where, B, NH, S, D, x_dtype, y_dtype, eps):
-    """Descriptor (as an argument) and the backward pass's workspace size."""
+    """Descriptor (as an argument) and the backward pass's workspace size, kept
+    by value: eps is a Python float."""
     desc = make_head_norm_desc(B, NH, S, D, x_dtype=_out_code(x_dtype, "x"), y_dtype=_out_code(y_dtype, "y_dtype"),
-                               eps=float(eps))
+                               eps=eps)
     st = head_norm_validate(desc)
     if st:
         raise MlstmError(st, where)
@@ -991,7 +998,7 @@ def head_norm_fw(x, weight=None, bias=None, *, eps: float = 1e-6, y_dtype=None, 
     _check_on(dev, "bias", bias, (NH, D), torch.float32)
     if out is not None:
         _check_on(dev, "y", out, (B, S, NH, D), y_dtype)
-    desc, _ = _norm_plan("mlstm_head_norm_fw", B, NH, S, D, x.dtype, y_dtype, eps)
+    desc, _ = _norm_plan("mlstm_head_norm_fw", B, NH, S, D, x.dtype, y_dtype, float(eps))
     y = x.new_empty((B, S, NH, D), dtype=y_dtype) if out is None else out
     _call("mlstm_head_norm_fw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y))
     return y
@@ -1014,7 +1021,7 @@ def _norm_grads(x, dy, weight, eps, weight_grad, bias_grad, workspace=None):
     torch = _torch()
     B, NH, S, D = x.shape
     dev = x.device
-    desc, need = _norm_plan("mlstm_head_norm_bw", B, NH, S, D, x.dtype, dy.dtype, eps)
+    desc, need = _norm_plan("mlstm_head_norm_bw", B, NH, S, D, x.dtype, dy.dtype, float(eps))
     dx, ws_bytes = torch.empty_like(x), 0
 
     def row():
@@ -1056,7 +1063,7 @@ def _head_norm_function():
 def head_norm(x, weight=None, bias=None, *, eps: float = 1e-6, y_dtype=None):
     """head_norm_fw as a torch autograd function (gradients for x, weight and
     bias by mlstm_head_norm_bw)."""
-    return _head_norm_function().apply(x, weight, bias, eps, y_dtype)
+    return _head_norm_function().apply(x, weight, bias, float(eps), y_dtype)
 
 
 def _normed(H, q, weight, bias, eps):
