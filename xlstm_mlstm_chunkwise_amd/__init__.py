@@ -214,6 +214,14 @@ def _check(t, name, shape, dtype=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _readable(grad):
+    """An incoming gradient as the kernels read it: contiguous and 16-byte
+    aligned.  (Autograd hands on views; behind a torch.cat they start at any
+    element.)"""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 def _stream():
     return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
 
@@ -695,7 +703,7 @@ def mlstm_chunkwise(q, k, v, i_pre, f_pre, C0=None, n0=None, m0=None, *, chunk_s
             q_, k_, v_, i_, f_, C0_, n0_, m0_ = ctx.saved_tensors[:8]
             saved = tuple(ctx.saved_tensors[8:]) or None
             want_state = any(ctx.needs_input_grad[5:])
-            g = mlstm_chunkwise_bw(q_, k_, v_, i_, f_, dH.contiguous().float(), C0_, n0_, m0_,
+            g = mlstm_chunkwise_bw(q_, k_, v_, i_, f_, _readable(dH.float()), C0_, n0_, m0_,
                                    state_grads=want_state, saved=saved, **kw)
             cast = lambda t, like: None if t is None else t.to(like.dtype)
             return (cast(g["dQ"], q_), cast(g["dK"], k_), cast(g["dV"], v_), g["d_i"], g["d_f"],
@@ -921,7 +929,7 @@ def _delta_function():
                     return (None,) * 9
                 if dH is None:
                     dH = torch.zeros(ctx.h_like[0], dtype=ctx.h_like[1], device=q.device)
-                g = mlstm_delta_bw(q, k, v, i_pre, f_pre, dH.contiguous(), C0, None if dC is None else dC.contiguous(),
+                g = mlstm_delta_bw(q, k, v, i_pre, f_pre, _readable(dH), C0, None if dC is None else dC.contiguous(),
                                    qk_scale=ctx.qk_scale, state_grads=ctx.needs_input_grad[5])
                 return g["dQ"], g["dK"], g["dV"], g["d_i"], g["d_f"], g.get("dC0"), None, None, None
 
@@ -1054,7 +1062,7 @@ def _head_norm_function():
                 x, weight = ctx.saved_tensors
                 _, need_w, need_b, _, _ = ctx.needs_input_grad
                 # the forward has checked x and weight, and dy has y's shape and type
-                return (*_norm_grads(x, dy.contiguous(), weight, ctx.eps, need_w, need_b), None, None)
+                return (*_norm_grads(x, _readable(dy), weight, ctx.eps, need_w, need_b), None, None)
 
         _functions["norm"] = HeadNorm
     return _functions["norm"]
