@@ -222,9 +222,11 @@ __global__ __launch_bounds__(kSumThreads) void head_norm_sum_kernel(const HeadNo
   constexpr int RUNS = kSumThreads / 64;
   __shared__ float s_run[RUNS][64];
   const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
-  const size_t n = (size_t)p.NH * 2 * p.D, i = (size_t)blockIdx.x * 64 + lane;
-  float s = 0.0f;
-  if (i < n)
+  const size_t n = (size_t)p.NH * 2 * p.D;
+  // the same trip count for every thread of a workgroup
+  for (size_t i0 = (size_t)blockIdx.x * 64; i0 < n; i0 += (size_t)gridDim.x * 64) {
+    const size_t i = i0 + lane;  // n is a multiple of 64
+    float s = 0.0f;
     for (int k = run; k < p.blocks; k += 4 * RUNS) {
       float x[4];
 #pragma unroll
@@ -232,14 +234,17 @@ __global__ __launch_bounds__(kSumThreads) void head_norm_sum_kernel(const HeadNo
 #pragma unroll
       for (int j = 0; j < 4; ++j) s += x[j];
     }
-  s_run[run][lane] = s;
-  __syncthreads();
-  if (run || i >= n) return;
+    s_run[run][lane] = s;
+    __syncthreads();
+    if (run == 0) {
 #pragma unroll
-  for (int k = 1; k < RUNS; ++k) s += s_run[k][lane];
-  const size_t h = i / (2 * p.D), which = i / p.D % 2, d = i % p.D;
-  float* out = which ? p.dbias : p.dweight;
-  if (out) out[h * p.D + d] = s;
+      for (int k = 1; k < RUNS; ++k) s += s_run[k][lane];
+      const size_t h = i / (2 * p.D), which = i / p.D % 2, d = i % p.D;
+      float* out = which ? p.dbias : p.dweight;
+      if (out) out[h * p.D + d] = s;
+    }
+    __syncthreads();  // the runs are read out
+  }
 }
 
 // Four rows a group where that leaves 2048 workgroups, eight a CU: 524288 rows
@@ -306,8 +311,11 @@ hipError_t launch_head_norm(const HeadNormParams& p, hipStream_t stream) { retur
 hipError_t launch_head_norm_back(const HeadNormParams& p, hipStream_t stream) {
   hipError_t e = launch(p, true, stream);
   if (e != hipSuccess || !p.partial) return e;
-  const size_t n = (size_t)p.NH * 2 * p.D;
-  hipLaunchKernelGGL(head_norm_sum_kernel, dim3((unsigned)((n + 63) / 64)), dim3(kSumThreads), 0, stream, p);
+  // 2^20 workgroups at most: a launch has to stay below 2^32 threads, which one
+  // a 64 sums would reach at NH D = 2^27
+  const size_t groups = (size_t)p.NH * 2 * p.D / 64, most = 1 << 20;
+  hipLaunchKernelGGL(head_norm_sum_kernel, dim3((unsigned)(groups < most ? groups : most)), dim3(kSumThreads), 0, stream,
+                     p);
   return hipGetLastError();
 }
 
