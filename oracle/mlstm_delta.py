@@ -70,7 +70,9 @@ def delta_grad(q, k, v, i_pre, f_pre, dH, C0=None, dC=None, qk_scale=None):
         dk[..., t, :] = np.matmul(G, (bt * r)[..., None])[..., 0] - at * np.matmul(before, dr[..., None])[..., 0]
         da[..., t] = (G * before).sum((-1, -2)) - (dr * _t(before, kt)).sum(-1)
         G = at[..., None] * (G - kt[..., :, None] * dr[..., None, :])
-    return dict(dQ=dq, dK=dk, dV=dv, d_i=db * b * (1 - b), d_f=da * a * (1 - a), dC0=G)
+    # 1 - sigmoid(x) as sigmoid(-x): near 1 the difference keeps no digits, in 64 bits either
+    return dict(dQ=dq, dK=dk, dV=dv, d_i=db * b * _sigmoid(-np.asarray(i_pre, np.float64)),
+                d_f=da * a * _sigmoid(-np.asarray(f_pre, np.float64)), dC0=G)
 
 
 def head_norm_fw(x, weight=None, bias=None, eps=1e-6):

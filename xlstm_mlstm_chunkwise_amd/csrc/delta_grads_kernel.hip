@@ -397,7 +397,8 @@ delta_grads_kernel(const DeltaParams p) {
       const bool closed = expf(log_sigmoid(f)) == 0.0f || (t0 + t == 0 && !p.C0 && f == f);
       p.d_f[o] = closed ? 0.0f : d / (1.0f + expf(f));
       const float beta = 1.0f / (1.0f + expf(-ip));
-      p.d_i[o] = beta == 0.0f ? 0.0f : s_dvu[t] / beta * (1.0f - beta);
+      // 1 - b as sigmoid(-i): subtracted from one it would keep no digits near b = 1
+      p.d_i[o] = beta == 0.0f ? 0.0f : s_dvu[t] / beta / (1.0f + expf(ip));
     }
   }
 }
