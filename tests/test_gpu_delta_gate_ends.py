@@ -66,3 +66,40 @@ def test_nearly_open(mt, DK, DV, kind):
     x, i, f, dH, C0, rng = _draw(DK + DV, DK, DV, kind)
     i[..., ::3] = 5.0 + 25.0 * rng.random(i[..., ::3].shape)
     _check(mt, kind, x, i, f, dH, C0, slice(None))
+
+
+@pytest.mark.parametrize("DK,DV,kind", [(64, 64, "bf16"), (128, 192, "bf16"), (256, 128, "bf16"), (64, 128, "f32"), (256, 64, "f32")])
+def test_nearly_closed(mt, DK, DV, kind):
+    """i down to -68: b^2 is far below the smallest float32 value, b's own
+    third parts (2^-16 b and the products with them) are not yet."""
+    x, i, f, dH, C0, rng = _draw(DK + DV + 1, DK, DV, kind)
+    i[..., ::3] = -68.0 + 48.0 * rng.random(i[..., ::3].shape)
+    _check(mt, kind, x, i, f, dH, C0, slice(None))
+
+
+def test_closed_and_almost(mt):
+    """Down to i = -120, where b is zero in float32.  dV and U carry b, in parts
+    of eight bits: with b below 2^-110 their last parts and then their middle
+    ones go below the smallest normal value, 2^-126, and the first keeps
+    2^-7; two products (T with dU, T with r, whose other terms at most double
+    them) make 4 2^-7 of |dU| |r|, and what is below 2^-126 may be lost."""
+    x, i, f, dH, C0, _ = _draw(3, 64, 64, "bf16")
+    i[..., 20:140] = np.linspace(-60.0, -120.0, 120)
+    args = [torch.from_numpy(a).to("cuda", torch.bfloat16) for a in x] + [torch.from_numpy(a).cuda() for a in (i, f)]
+    got = mt.mlstm_delta_bw(*args, torch.from_numpy(dH).to("cuda", torch.bfloat16), torch.from_numpy(C0).cuda())["d_i"]
+    want = delta_grad(*x, i, f, dH, C0)
+    z = i.astype(np.float64)
+    b, a = 1.0 / (1.0 + np.exp(-z)), 1.0 / (1.0 + np.exp(-f.astype(np.float64)))
+    du, r, C = want["dV"] / b[..., None], np.empty_like(want["dV"]), C0.astype(np.float64)
+    for t in range(S):
+        k = x[1][..., t, :].astype(np.float64)
+        r[..., t, :] = x[2][..., t, :] - a[..., t, None] * np.matmul(k[..., None, :], C)[..., 0, :]
+        C = a[..., t, None, None] * C + k[..., None] * (b[..., t, None] * r[..., t, :])[..., None, :]
+    assert np.allclose((du * r).sum(-1) * b * (1.0 - b), want["d_i"])
+    size = np.linalg.norm(du, axis=-1) * np.linalg.norm(r, axis=-1)
+    lost = 2.0 ** -126 * (np.abs(du).sum(-1) + np.abs(r).sum(-1))
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    off = (np.abs(got - want["d_i"]) - 4 * 2.0 ** -7 * b * size - lost)[..., 20:140]
+    assert off.max() <= 0, float(off.max())
+    assert (got[i < -104.0] == 0).all()

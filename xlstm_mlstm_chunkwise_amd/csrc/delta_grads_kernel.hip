@@ -7,7 +7,7 @@
 //   dQ = s e dH C^T + dP K,
 //   dK = dP^T Q + (dA + dA^T) K - e dV C^T + w U G^T,
 //   d log a_t = sum_{r >= t} (q_r . dq_r - v_r . dv_r) + <C behind, G>,
-//   d b_t = dV_t . U_t / b_t^2,
+//   d i_t = (1 - b_t) dV_t . (U_t / b_t),
 // with the sum over the chunk's own rows only and <C behind, G> = g <C, G> +
 // sum_t w_t u_t . (K G)_t formed afresh for every chunk: one running sum over
 // the whole sequence would add up the roundings of all tokens behind t.
@@ -20,9 +20,10 @@
 // terms of dK add into one accumulator.  Every load is issued a step ahead:
 // without that the step took the latency of memory three times over.
 //
-// 64 heads of 256 x 512 at 8192 tokens: 2.70-2.81 ms for 12.4 GB (4.5 TB/s; a
+// 64 heads of 256 x 512 at 8192 tokens: 2.85 ms for 12.4 GB (4.4 TB/s; a
 // large copy reaches 5.1), two thirds of them the states.  64 heads of 128 x 128 at
-// 2048 tokens: 164-171 us; 15 of 64 x 192 at 1777 tokens: 34 us.
+// 2048 tokens: 170 us; 15 of 64 x 192 at 1777 tokens: 34 us.  (1 / b in every
+// term of d i: 1.4 % of the first, nothing of the others.)
 #include "delta_common.h"
 #include "kernels.h"
 
@@ -136,7 +137,7 @@ delta_grads_kernel(const DeltaParams p) {
     for (int j = 0; j < RT; ++j) dq[i][j] = dk[i][j] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < TPW; ++i) hu[i] = ru[i] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-  float cg = 0.0f, dvu[ROWS], vdv[ROWS], qe[ROWS], qw[ROWS];
+  float cg = 0.0f, dvu[ROWS], vdv[ROWS], qe[ROWS], qw[ROWS], qb[ROWS];
 
   // this wave's rows of the states, this thread's quads of the rest
   const uint32_t rows_bytes = 16u * KPW * (uint32_t)DV * 4u;
@@ -173,7 +174,7 @@ delta_grads_kernel(const DeltaParams p) {
       const float4_t u = qu[i].values(), r = qr[i].values(), v = qv[i].values();
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        dvu[i] += r[e] * u[e];
+        dvu[i] += r[e] * (qb[i] * u[e]);
         vdv[i] += v[e] * r[e];
       }
       if (QUADS % THREADS != 0 && quad >= QUADS) continue;
@@ -193,6 +194,10 @@ delta_grads_kernel(const DeltaParams p) {
     dvu[i] = vdv[i] = 0.0f;
     qe[i] = -p.e[at * L + t];
     qw[i] = p.w[at * L + t];
+    // 1 / b, for rows with a b: both dV and U carry it, and b^2 is below the
+    // smallest float32 value from i = -44 down
+    const float inv = t0 + t < p.S ? 1.0f + expf(-p.i_pre[(size_t)bh * p.S + t0 + t]) : 0.0f;
+    qb[i] = inv == INFINITY ? 0.0f : inv;
   }
   fetch(0);
   xc.load(r_c, state_off, row16, 0);
@@ -398,7 +403,7 @@ delta_grads_kernel(const DeltaParams p) {
       p.d_f[o] = closed ? 0.0f : d / (1.0f + expf(f));
       const float beta = 1.0f / (1.0f + expf(-ip));
       // 1 - b as sigmoid(-i): subtracted from one it would keep no digits near b = 1
-      p.d_i[o] = beta == 0.0f ? 0.0f : s_dvu[t] / beta / (1.0f + expf(ip));
+      p.d_i[o] = beta == 0.0f ? 0.0f : s_dvu[t] / (1.0f + expf(ip));
     }
   }
 }
