@@ -550,11 +550,22 @@ int mlstm_bw_grads(const mlstm_fw_desc_t* desc,
  * of padding therefore have to be finite (zeros with i_t = -inf write
  * nothing), and in the backward pass their dH too.
  *
- * Arithmetic: every operand computed in float32 (the state, U, the inverse
- * within a chunk) enters the bf16 matrix cores in three parts of eight bits,
- * float32 inputs too; products accumulate in float32, the sums of log a
- * within a chunk in double.  Terms of dQ and dK that are stored as bf16 use
- * two parts where nothing else reads them. */
+ * Arithmetic: products run on the bf16 matrix cores and accumulate in float32;
+ * the sums of log a within a chunk are taken in double.  bf16 Q, K, V and dH
+ * enter as they are, float32 ones and every operand computed in float32 (the
+ * state, U, dV, the inverse within a chunk) in three parts of eight bits; of a
+ * product of two such operands, terms below 2^-21 of it are left out.  Two
+ * outputs take fewer parts, because eight bits of them are stored:
+ *   H in bf16     the state in two truncated parts (off by less than 2^-15),
+ *                 the weights within the chunk and U in two rounded ones
+ *                 (2^-18).  About one value in 200 becomes the other
+ *                 neighbour of the one that a float32 H would be rounded to.
+ *   dK in bf16    all its operands in two parts; one value in 150.
+ * The final state, dQ, dV, d_i, d_f and dC0 have three parts whatever the types.
+ * d_i keeps its digits at a nearly open input gate, and at a nearly closed one
+ * down to i_t = -68, where the parts of what carries b begin to leave float32's
+ * range; d_f is a difference of sums over the chunk and has the digits of those
+ * sums, also where it is smaller. */
 typedef struct {
   int32_t B, NH;       /* batch, heads: >= 1; B * NH * ceil(S / 32) and
                           B * NH * DHV / 64 below 2^23                        */

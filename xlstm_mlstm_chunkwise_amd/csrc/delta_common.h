@@ -6,11 +6,14 @@
 // A product of an n-part and an m-part operand runs the part pairs (i, j)
 // with i + j < max(n, m): a bf16 input (one part) times a three-part operand
 // takes three matrix instructions and loses nothing but the float32
-// accumulation; three parts times three take six and drop terms below 2^-24.
+// accumulation; three parts times three take six and drop mid x lo twice.  The
+// parts are truncated, so mid is below 2^-7 and lo below 2^-15 of the leading
+// power of two: the two dropped terms are below 2^-21 of the product, always of
+// its sign, and about 2^-23 on average.
 // The state is carried from chunk to chunk in float32 and every chunk
 // multiplies it, so two-part operands (2^-17 a rounding) would show in the
 // float32 outputs (final state, gate gradients: 4e-6 to 9e-6 of their norm
-// instead of below 1e-6); only results that are stored as bf16 use two.
+// instead of below 1e-6); only results that are stored as bf16 (H, dK) use two.
 #pragma once
 
 #include "device_common.h"

@@ -4,13 +4,14 @@
 //   u = b (v - a C^T k),   C' = a C + k u^T,   h = s C'^T q.
 // h = s (a C^T q + u (k . q)), so one pass over C gives both C^T k and
 // C^T q, and C' is written from the registers that hold C: the state is read
-// once and written once, which bounds the step.  One workgroup per (head, 128
-// or 64 columns): thread (row group, column quad) holds 16-byte pieces of
+// once and written once, which bounds the step.  One workgroup per (head, 64
+// columns): thread (row group, column quad) holds 16-byte pieces of
 // every 16th row, all loads issued before anything waits on them, with
 // non-temporal accesses as in the step of the plain cell (a model's other
 // layers pass through the caches between two steps of one layer).  64 heads
-// of 256 x 512: 11.6 us for 67.5 MB (5.8 TB/s); with 128 columns a workgroup
-// 12.1 us.
+// of 256 x 512, 67.5 MB: 13.5 us with states that no cache holds (twelve sets in
+// turn, 5.0 TB/s), 11.2 us on the same set again and again; on that, 128 columns
+// a workgroup took 12.1 us against 11.6.
 #include "device_common.h"
 #include "kernels.h"
 
