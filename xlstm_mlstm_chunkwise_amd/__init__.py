@@ -854,7 +854,9 @@ def mlstm_delta_bw(q, k, v, i_pre, f_pre, dH, C0=None, dC=None, *, qk_scale: Opt
     f_pre, C0).  dH has H's shape, bfloat16 or float32; dC (B, NH, DHQK, DHV)
     float32 or None (no gradient enters through the final state).  Returns a
     dict with dQ, dK, dV (q's dtype), d_i, d_f (float32) and, with
-    state_grads, dC0 (float32)."""
+    state_grads, dC0 (float32).  The workspace, delta_bw_workspace_bytes of
+    the descriptor (two float32 states for every 64 tokens, 32 for float32
+    inputs, and more), is allocated here unless it is given."""
     torch = _torch()
     B, NH, S, DK, DV = _delta_inputs(q, k, v, i_pre, f_pre, C0)
     dev = q.device
