@@ -153,7 +153,7 @@ def _own(st):
         grads = torch.autograd.grad(y, st["leaves"], st["dy"])
         return {"y": y.detach(), **dict(zip(("dx", "dw", "db", "ds0"), grads))}
     if op == "dropout":
-        y = mt.dropout(st["x"], st["p"], st["seed"], st["offset"], residual=st["r"])
+        y = mt.dropout(st["x"], st["p"], st["seed"] % 2 ** 64, st["offset"] % 2 ** 64, residual=st["r"])
         dx, dr = torch.autograd.grad(y, st["leaves"], st["dy"])
         return {"y": y.detach(), "dx": dx, "dr": dr}
     args = [st[n] for n in ("x", "dt", "A", "Bm", "Cm", "Dm", "z", "bias", "h0")]
