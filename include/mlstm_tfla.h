@@ -675,6 +675,178 @@ int mlstm_head_norm_bw(const mlstm_head_norm_desc_t* desc,
                        void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around a recurrent cell of a block, and the cell with a
+ * diagonal state.  Tensors have the channels last, (B, S, D), as the
+ * projections in front of them and behind them do.
+ *
+ * A "view" input may be a run of columns of a wider tensor (half of a
+ * projection's output): its channels are adjacent, and the descriptor has its
+ * strides in elements, from one sequence to the next and from one token to the
+ * next; 0 stands for the stride of a contiguous tensor.  The token's stride is
+ * at least the number of columns (tokens do not overlap) and below 2^26.  Such
+ * inputs need the alignment of one element only.  Everything else is contiguous.
+ *
+ * Short causal convolution, every channel by itself, K taps:
+ *
+ *   xe = [state, x]                      (K - 1 + S rows of D channels)
+ *   p_t = bias + sum_k weight[., k] xe_{t+k},   y_t = p_t sigmoid(p_t)  (silu)
+ *                                               y_t = p_t               (else)
+ *   state' = the last K - 1 rows of xe
+ *
+ * Sums in float32.  A non-finite x reaches the K rows that its taps reach. */
+typedef struct {
+  int32_t B, S, D;     /* B, D >= 1, S >= 0; B * (S + 3) * D below 2^40,
+                          B * (S + 3) below 2^32, S below 2^30, D below
+                          2^26, B below 2^16                                  */
+  int32_t K;           /* taps: 2, 3 or 4                                     */
+  int32_t dtype;       /* mlstm_dtype_t of x, y, the states, and gradients    */
+  int32_t silu;        /* 1: y = p sigmoid(p); 0: y = p                       */
+  int64_t x_strides[2];/* view x: batch, token                                */
+  int32_t reserved[4]; /* must be zero                                        */
+} mlstm_conv_desc_t;
+
+int mlstm_conv_validate(const mlstm_conv_desc_t* desc);
+
+/* Bytes of device workspace of mlstm_conv_bw when dweight or dbias is asked
+ * for (partial sums); 0 for an invalid descriptor. */
+size_t mlstm_conv_bw_workspace_bytes(const mlstm_conv_desc_t* desc);
+
+/*   x         (B, S, D) dtype, a view
+ *   weight    (D, K) float32, bias (D) float32 (may be NULL: zero)
+ *   state     (B, K - 1, D) dtype, may be NULL: zeros
+ *   y         (B, S, D) dtype
+ *   state_out (B, K - 1, D) dtype, may be NULL: not written */
+int mlstm_conv_fw(const mlstm_conv_desc_t* desc,
+                  const void* x, const float* weight, const float* bias, const void* state,
+                  void* y, void* state_out, void* stream);
+
+/* Gradients of sum(dy * y) + sum(dstate_out * state_out).  dy (B, S, D) and
+ * dx (B, S, D) dtype; dstate_out (B, K - 1, D) dtype, may be NULL: zero;
+ * dstate (B, K - 1, D) dtype, dweight (D, K), dbias (D) float32, each may be
+ * NULL (not written); without the last two no workspace is needed.  p is
+ * formed again.  Equal inputs give equal bits. */
+int mlstm_conv_bw(const mlstm_conv_desc_t* desc,
+                  const void* x, const float* weight, const float* bias, const void* state,
+                  const void* dy, const void* dstate_out,
+                  void* dx, void* dstate, float* dweight, float* dbias,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token; S must be 1 (else MLSTM_E_SHAPE): x (B, D), a view with the
+ * batch stride alone, y (B, D).  state_out is required and may be state itself
+ * (updated in place). */
+int mlstm_conv_step(const mlstm_conv_desc_t* desc,
+                    const void* x, const float* weight, const float* bias, const void* state,
+                    void* y, void* state_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Selective scan: a recurrence with N states a channel, each with a decay of
+ * its own that the token sets.  With d = softplus(dt + dt_bias):
+ *
+ *   h_t[c, n] = exp(d_t[c] A[c, n]) h_{t-1}[c, n] + d_t[c] x_t[c] Bm_t[n]
+ *   r_t[c]    = sum_n Cm_t[n] h_t[c, n] + Dskip[c] x_t[c]
+ *   y_t[c]    = r_t[c] z_t[c] sigmoid(z_t[c])           (z given; else r_t[c])
+ *
+ * States, sums and products in float32.  dt = -inf leaves the state as it is
+ * (d = 0) where x and Bm are finite.  A non-finite x, dt or z stays in its
+ * channel (from its token on; in the backward pass dBm, dCm of the token have
+ * it too); a non-finite Bm or Cm reaches every channel. */
+typedef struct {
+  int32_t B, S, D;     /* B, D >= 1, S >= 0; B * S * D below 2^40, S below
+                          2^30, D below 2^26, B * ceil(D / 64) below 2^20     */
+  int32_t N;           /* states a channel: 16, 32 or 64                      */
+  int32_t dtype;       /* mlstm_dtype_t of x, dt, Bm, Cm, z, y and gradients  */
+  int32_t reserved0;   /* must be zero                                        */
+  int64_t x_strides[2], dt_strides[2], z_strides[2], B_strides[2], C_strides[2];
+                       /* views: batch, token                                 */
+  int32_t reserved[4]; /* must be zero                                        */
+} mlstm_scan_desc_t;
+
+int mlstm_scan_validate(const mlstm_scan_desc_t* desc);
+
+/* Bytes of device workspace; 0 for an invalid descriptor.  Forward: Bm and Cm
+ * in float32 and, where the sequence is cut into chunks that are walked side by
+ * side, a state and a float a channel for each.  Backward: also the state in
+ * front of every eight tokens and, for every 128 channels, a part of dBm and
+ * dCm, all in float32. */
+size_t mlstm_scan_fw_workspace_bytes(const mlstm_scan_desc_t* desc);
+size_t mlstm_scan_bw_workspace_bytes(const mlstm_scan_desc_t* desc);
+
+/*   x, dt, z  (B, S, D) dtype, views; z may be NULL
+ *   A         (D, N) float32, 16-byte aligned
+ *   Bm, Cm    (B, S, N) dtype, views
+ *   Dskip, dt_bias  (D) float32, may be NULL (zeros)
+ *   h0        (B, D, N) float32, 16-byte aligned, may be NULL: zero state
+ *   y         (B, S, D) dtype
+ *   h_out     (B, D, N) float32, 16-byte aligned, may be NULL: not written
+ *   workspace at least mlstm_scan_fw_workspace_bytes(desc) bytes, 256-byte
+ *             aligned; may be NULL when that is 0.
+ * With S == 0 the call only writes h_out. */
+int mlstm_scan_fw(const mlstm_scan_desc_t* desc,
+                  const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                  const float* Dskip, const void* z, const float* dt_bias, const float* h0,
+                  void* y, float* h_out,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(dy * y) + sum(dh_out * h_out).
+ *   dy            (B, S, D) dtype
+ *   dh_out        (B, D, N) float32, 16-byte aligned, may be NULL: zero
+ *   dx, ddt       (B, S, D) dtype; dz the same, required with z and NULL without
+ *   dBm, dCm      (B, S, N) dtype
+ *   dA            (D, N) float32, 16-byte aligned
+ *   dDskip, dbias (D) float32, may be NULL
+ *   dh0           (B, D, N) float32, 16-byte aligned, may be NULL
+ * The forward quantities are formed again.  Sums are taken in a fixed order:
+ * equal inputs give equal bits.  With S == 0 dA, dDskip and dbias are zeros,
+ * and dh0 is dh_out. */
+int mlstm_scan_bw(const mlstm_scan_desc_t* desc,
+                  const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                  const float* Dskip, const void* z, const float* dt_bias, const float* h0,
+                  const void* dy, const float* dh_out,
+                  void* dx, void* ddt, float* dA, void* dBm, void* dCm,
+                  float* dDskip, void* dz, float* dbias, float* dh0,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token; S must be 1 (else MLSTM_E_SHAPE): x, dt, z (B, D), Bm, Cm (B, N),
+ * views with the batch stride alone.  h_out is required and may be h_in itself
+ * (updated in place); h_in may be NULL: zero state. */
+int mlstm_scan_step(const mlstm_scan_desc_t* desc,
+                    const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                    const float* Dskip, const void* z, const float* dt_bias, const float* h_in,
+                    void* y, float* h_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Dropout whose mask is formed where it is needed and never stored, with the
+ * residual sum behind it:
+ *
+ *   y_i = x_i / (1 - p) + residual_i   where value i is kept
+ *   y_i = residual_i                   where it is dropped
+ *
+ * Value i is dropped where word i % 4 of Philox 4x32 with ten rounds (Salmon,
+ * Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011),
+ * key = seed and counter = (i / 4, offset), 64 bits each, low word first, is
+ * below floor(p 2^32).  The gradient for x is the same call on dy, without a
+ * residual; the gradient for the residual is dy.  A dropped value may be
+ * anything, NaN included. */
+typedef struct {
+  int64_t n;           /* values: 0 .. 2^40                                   */
+  int64_t seed, offset;/* their 64 bits, whatever the sign                    */
+  double p;            /* 0 <= p < 1                                          */
+  int32_t dtype;       /* mlstm_dtype_t of x, residual and y                  */
+  int32_t reserved[3]; /* must be zero                                        */
+} mlstm_dropout_desc_t;
+
+int mlstm_dropout_validate(const mlstm_dropout_desc_t* desc);
+
+/*   x, y      n values, dtype; y may be x itself
+ *   residual  n values, dtype, may be NULL; y may be residual itself
+ *   seed_dev  may be NULL; else two int64 in device memory, 8-byte aligned,
+ *             read when the call runs on its stream in place of desc->seed and
+ *             desc->offset (so that a captured call can be replayed with
+ *             others). */
+int mlstm_dropout(const mlstm_dropout_desc_t* desc,
+                  const void* x, const void* residual, const int64_t* seed_dev, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

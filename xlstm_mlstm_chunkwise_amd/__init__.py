@@ -1,6 +1,7 @@
 """MI355X (gfx950) chunkwise mLSTM: Python binding of libmlstm_tfla.so (forward
 pass, backward pass and recurrent decode step; the same of the gated delta
-rule; the head norm behind either).
+rule, of the selective scan and of the short causal convolution in front of a
+cell; the head norm behind the first two; dropout with the residual sum).
 
 The binding only marshals arguments: it allocates outputs and workspace with
 PyTorch (device memory), passes raw device pointers and the current HIP
@@ -74,6 +75,33 @@ class HeadNormDesc(ctypes.Structure):
     ]
 
 
+class ConvDesc(ctypes.Structure):
+    """Mirror of mlstm_conv_desc_t."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("S", ctypes.c_int32), ("D", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32), ("x_strides", ctypes.c_int64 * 2),
+        ("reserved", ctypes.c_int32 * 4),
+    ]
+
+
+class ScanDesc(ctypes.Structure):
+    """Mirror of mlstm_scan_desc_t."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("S", ctypes.c_int32), ("D", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("reserved0", ctypes.c_int32), ("x_strides", ctypes.c_int64 * 2),
+        ("dt_strides", ctypes.c_int64 * 2), ("z_strides", ctypes.c_int64 * 2), ("B_strides", ctypes.c_int64 * 2),
+        ("C_strides", ctypes.c_int64 * 2), ("reserved", ctypes.c_int32 * 4),
+    ]
+
+
+class DropoutDesc(ctypes.Structure):
+    """Mirror of mlstm_dropout_desc_t."""
+    _fields_ = [
+        ("n", ctypes.c_int64), ("seed", ctypes.c_int64), ("offset", ctypes.c_int64), ("p", ctypes.c_double),
+        ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32 * 3),
+    ]
+
+
 _lib = None
 _SYMBOLS = {
     "mlstm_abi_version": (ctypes.c_int, []),
@@ -119,6 +147,22 @@ _SYMBOLS = {
     "mlstm_head_norm_fw": (ctypes.c_int, [ctypes.POINTER(HeadNormDesc)] + [ctypes.c_void_p] * 5),
     "mlstm_head_norm_bw": (ctypes.c_int, [ctypes.POINTER(HeadNormDesc)] + [ctypes.c_void_p] * 7
                            + [ctypes.c_size_t, ctypes.c_void_p]),
+    "mlstm_conv_validate": (ctypes.c_int, [ctypes.POINTER(ConvDesc)]),
+    "mlstm_conv_bw_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(ConvDesc)]),
+    "mlstm_conv_fw": (ctypes.c_int, [ctypes.POINTER(ConvDesc)] + [ctypes.c_void_p] * 7),
+    "mlstm_conv_bw": (ctypes.c_int, [ctypes.POINTER(ConvDesc)] + [ctypes.c_void_p] * 11
+                      + [ctypes.c_size_t, ctypes.c_void_p]),
+    "mlstm_conv_step": (ctypes.c_int, [ctypes.POINTER(ConvDesc)] + [ctypes.c_void_p] * 7),
+    "mlstm_scan_validate": (ctypes.c_int, [ctypes.POINTER(ScanDesc)]),
+    "mlstm_scan_fw_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(ScanDesc)]),
+    "mlstm_scan_bw_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(ScanDesc)]),
+    "mlstm_scan_fw": (ctypes.c_int, [ctypes.POINTER(ScanDesc)] + [ctypes.c_void_p] * 12
+                      + [ctypes.c_size_t, ctypes.c_void_p]),
+    "mlstm_scan_bw": (ctypes.c_int, [ctypes.POINTER(ScanDesc)] + [ctypes.c_void_p] * 21
+                      + [ctypes.c_size_t, ctypes.c_void_p]),
+    "mlstm_scan_step": (ctypes.c_int, [ctypes.POINTER(ScanDesc)] + [ctypes.c_void_p] * 12),
+    "mlstm_dropout_validate": (ctypes.c_int, [ctypes.POINTER(DropoutDesc)]),
+    "mlstm_dropout": (ctypes.c_int, [ctypes.POINTER(DropoutDesc)] + [ctypes.c_void_p] * 5),
 }
 
 
@@ -1082,3 +1126,430 @@ def _normed(H, q, weight, bias, eps):
             raise ValueError("norm_bias needs norm_weight")
         return H
     return head_norm(H, weight, bias, eps=eps, y_dtype=q.dtype)
+
+
+# ---------------------------------------------------------------------------
+# views: (B, S, columns) tensors that may be a run of columns of a wider one
+
+def _view(dev, name, t, shape, dtype):
+    """Strides in elements of t from a sequence to the next and from a token to
+    the next (its last axis has to be adjacent), 0 where only one is there; for
+    (B, columns), one token, the first of them.  None passes."""
+    if t is None:
+        return (0, 0)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.is_contiguous():
+        return (0, 0)
+    strides, shape = t.stride(), t.shape
+    if shape[-1] > 1 and strides[-1] != 1:
+        raise ValueError(f"{name}: its last axis must be adjacent in memory")
+    strides = tuple(0 if n <= 1 else s for s, n in zip(strides[:-1], shape[:-1]))
+    if any(s <= 0 and n > 1 for s, n in zip(strides, shape)) or 0 < strides[-1] < shape[-1]:
+        raise ValueError(f"{name} is broadcast or overlaps itself; make it contiguous")
+    return strides if len(strides) == 2 else (strides[0], 0)
+
+
+def _gpu_input(x, dims, layout):
+    if x.dim() != dims:
+        raise ValueError(f"x must be {layout}")
+    _out_code(x.dtype, "x")
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    return x.device
+
+
+# ---------------------------------------------------------------------------
+# short causal convolution
+
+def make_conv_desc(B, S, D, K, *, dtype=MLSTM_F32, silu=1, x_strides=(0, 0)) -> ConvDesc:
+    d = ConvDesc()
+    d.B, d.S, d.D, d.K, d.dtype, d.silu = B, S, D, K, dtype, silu
+    d.x_strides[:] = x_strides
+    return d
+
+
+def conv_validate(desc: ConvDesc) -> int:
+    return lib().mlstm_conv_validate(ctypes.byref(desc))
+
+
+def conv_bw_workspace_bytes(desc: ConvDesc) -> int:
+    return lib().mlstm_conv_bw_workspace_bytes(ctypes.byref(desc))
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_plan(where, B, S, D, K, dtype, activation, x_strides):
+    """Descriptor (as an argument) and the backward pass's workspace size, kept
+    by value."""
+    if activation not in (None, "silu"):
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    desc = make_conv_desc(B, S, D, K, dtype=_out_code(dtype, "x"), silu=int(activation == "silu"), x_strides=x_strides)
+    st = conv_validate(desc)
+    if st:
+        raise MlstmError(st, where)
+    return ctypes.byref(desc), conv_bw_workspace_bytes(desc)
+
+
+def _conv_inputs(where, x, weight, bias, state, activation):
+    torch = _torch()
+    dev = _gpu_input(x, 3, "(B, S, D)")
+    B, S, D = x.shape
+    if weight.dim() != 2:
+        raise ValueError("weight must be (D, K)")
+    K = weight.shape[1]
+    _check_on(dev, "weight", weight, (D, K), torch.float32)
+    _check_on(dev, "bias", bias, (D,), torch.float32)
+    _check_on(dev, "state", state, (B, K - 1, D), x.dtype)
+    desc, need = _conv_plan(where, B, S, D, K, x.dtype, activation, _view(dev, "x", x, x.shape, x.dtype))
+    return dev, B, S, D, K, desc, need
+
+
+def causal_conv_fw(x, weight, bias=None, state=None, *, activation: Optional[str] = None, out=None,
+                   return_final_state: bool = True):
+    """Short causal convolution of every channel on the GPU (mlstm_conv_fw).
+
+    x: (B, S, D) bfloat16 or float32, contiguous or a run of columns of a wider
+    tensor; weight (D, K) float32, K 2 to 4, the last tap on the token itself;
+    bias (D) float32 or None; state (B, K - 1, D) in x's dtype, the inputs in
+    front of x, or None (zeros); activation None or "silu".  Returns (y, state'),
+    state' None when return_final_state is False."""
+    torch = _torch()
+    dev, B, S, D, K, desc, _ = _conv_inputs("mlstm_conv_fw", x, weight, bias, state, activation)
+    _check_on(dev, "y", out, (B, S, D), x.dtype)
+    y = torch.empty((B, S, D), dtype=x.dtype, device=dev) if out is None else out
+    state_out = torch.empty((B, K - 1, D), dtype=x.dtype, device=dev) if return_final_state else None
+    _call("mlstm_conv_fw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out))
+    return y, state_out
+
+
+def causal_conv_bw(x, weight, dy, bias=None, state=None, dstate=None, *, activation: Optional[str] = None,
+                   weight_grads: bool = True, state_grads: bool = False, workspace=None):
+    """Backward pass of causal_conv_fw on the GPU (mlstm_conv_bw): a dict with
+    dx (x's dtype), with weight_grads dw (D, K) and db (D) in float32, and with
+    state_grads dstate.  dy has y's shape and x's dtype; dstate (B, K - 1, D) is
+    the gradient of the final state, or None."""
+    torch = _torch()
+    dev, B, S, D, K, desc, need = _conv_inputs("mlstm_conv_bw", x, weight, bias, state, activation)
+    _check_on(dev, "dy", dy, (B, S, D), x.dtype)
+    _check_on(dev, "dstate", dstate, (B, K - 1, D), x.dtype)
+    g = dict(dx=torch.empty((B, S, D), dtype=x.dtype, device=dev))
+    ws_bytes = 0
+    if weight_grads:
+        g["dw"] = torch.empty_like(weight)
+        g["db"] = torch.empty((D,), dtype=torch.float32, device=dev)
+        workspace, ws_bytes = _bytes_of(need, workspace, dev)
+    if state_grads:
+        g["dstate"] = torch.empty((B, K - 1, D), dtype=x.dtype, device=dev)
+    _call("mlstm_conv_bw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(dy), _ptr(dstate),
+          _ptr(g["dx"]), _ptr(g.get("dstate")), _ptr(g.get("dw")), _ptr(g.get("db")),
+          _ptr(workspace) if weight_grads else None, ws_bytes)
+    return g
+
+
+def causal_conv_step(x, weight, bias=None, state=None, *, activation: Optional[str] = None, state_out=None):
+    """One token of causal_conv_fw on the GPU (mlstm_conv_step): x (B, D), state
+    (B, K - 1, D) or None (zeros).  Returns (y, state'); state_out may be state
+    itself (updated in place)."""
+    torch = _torch()
+    dev = _gpu_input(x, 2, "(B, D)")
+    B, D = x.shape
+    if weight.dim() != 2:
+        raise ValueError("weight must be (D, K)")
+    K = weight.shape[1]
+    _check_on(dev, "weight", weight, (D, K), torch.float32)
+    _check_on(dev, "bias", bias, (D,), torch.float32)
+    _check_on(dev, "state", state, (B, K - 1, D), x.dtype)
+    _check_on(dev, "state_out", state_out, (B, K - 1, D), x.dtype)
+    desc, _ = _conv_plan("mlstm_conv_step", B, 1, D, K, x.dtype, activation, _view(dev, "x", x, x.shape, x.dtype))
+    y = torch.empty((B, D), dtype=x.dtype, device=dev)
+    if state_out is None:
+        state_out = torch.empty((B, K - 1, D), dtype=x.dtype, device=dev)
+    _call("mlstm_conv_step", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out))
+    return y, state_out
+
+
+def _conv_function():
+    """The autograd function of causal_conv."""
+    torch = _torch()
+    if "conv" not in _functions:
+        class CausalConv(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, weight, bias, state, activation, final_state):
+                y, s = causal_conv_fw(x, weight, bias, state, activation=activation, return_final_state=final_state)
+                ctx.save_for_backward(x, weight, bias, state)
+                ctx.set_materialize_grads(False)
+                ctx.activation = activation
+                return (y, s) if final_state else y
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy, ds=None):
+                x, weight, bias, state = ctx.saved_tensors
+                if dy is None and ds is None:
+                    return (None,) * 6
+                dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _readable(dy)
+                need = ctx.needs_input_grad
+                g = causal_conv_bw(x, weight, dy, bias, state, None if ds is None else _readable(ds),
+                                   activation=ctx.activation, weight_grads=need[1] or need[2], state_grads=need[3])
+                return (g["dx"], g.get("dw"), g.get("db") if bias is not None else None, g.get("dstate"), None, None)
+
+        _functions["conv"] = CausalConv
+    return _functions["conv"]
+
+
+def causal_conv(x, weight, bias=None, state=None, *, activation: Optional[str] = None, return_final_state: bool = False):
+    """causal_conv_fw as a torch autograd function (gradients for x, weight,
+    bias and state by mlstm_conv_bw).  Returns y, or (y, state') with
+    return_final_state; gradients flow in through both."""
+    return _conv_function().apply(x, weight, bias, state, activation, return_final_state)
+
+
+# ---------------------------------------------------------------------------
+# selective scan
+
+def make_scan_desc(B, S, D, N, *, dtype=MLSTM_F32, x_strides=(0, 0), dt_strides=(0, 0), z_strides=(0, 0),
+                   B_strides=(0, 0), C_strides=(0, 0)) -> ScanDesc:
+    d = ScanDesc()
+    d.B, d.S, d.D, d.N, d.dtype = B, S, D, N, dtype
+    d.x_strides[:], d.dt_strides[:], d.z_strides[:] = x_strides, dt_strides, z_strides
+    d.B_strides[:], d.C_strides[:] = B_strides, C_strides
+    return d
+
+
+def scan_validate(desc: ScanDesc) -> int:
+    return lib().mlstm_scan_validate(ctypes.byref(desc))
+
+
+def scan_fw_workspace_bytes(desc: ScanDesc) -> int:
+    return lib().mlstm_scan_fw_workspace_bytes(ctypes.byref(desc))
+
+
+def scan_bw_workspace_bytes(desc: ScanDesc) -> int:
+    return lib().mlstm_scan_bw_workspace_bytes(ctypes.byref(desc))
+
+
+@functools.lru_cache(maxsize=256)
+def _scan_plan(where, B, S, D, N, dtype, strides):
+    """Descriptor (as an argument) and workspace sizes, forward and backward,
+    kept by value."""
+    desc = make_scan_desc(B, S, D, N, dtype=_out_code(dtype, "x"), x_strides=strides[0], dt_strides=strides[1],
+                          z_strides=strides[2], B_strides=strides[3], C_strides=strides[4])
+    st = scan_validate(desc)
+    if st:
+        raise MlstmError(st, where)
+    return ctypes.byref(desc), scan_fw_workspace_bytes(desc), scan_bw_workspace_bytes(desc)
+
+
+def _scan_inputs(where, x, dt, A, B, C, D, z, dt_bias, h0):
+    """Plan of the call and the sizes, checked; x is (B, S, D), or (B, D) for
+    one token."""
+    torch = _torch()
+    if A.dim() != 2:
+        raise ValueError("A must be (D, N)")
+    dev, dtype, rows, (ch, N) = x.device, x.dtype, tuple(x.shape[:-1]), A.shape
+    cols = rows + (N,)
+    _check_on(dev, "A", A, (x.shape[-1], N), torch.float32)
+    strides = (_view(dev, "x", x, x.shape, dtype), _view(dev, "dt", dt, x.shape, dtype),
+               _view(dev, "z", z, x.shape, dtype), _view(dev, "B", B, cols, dtype), _view(dev, "C", C, cols, dtype))
+    _check_on(dev, "D", D, (ch,), torch.float32)
+    _check_on(dev, "dt_bias", dt_bias, (ch,), torch.float32)
+    _check_on(dev, "h0", h0, (rows[0], ch, N), torch.float32)
+    S = rows[1] if len(rows) == 2 else 1
+    return dev, rows[0], S, ch, N, _scan_plan(where, rows[0], S, ch, N, dtype, strides)
+
+
+def selective_scan_fw(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, out=None,
+                      return_final_state: bool = True, workspace=None):
+    """Selective scan on the GPU (mlstm_scan_fw): with d = softplus(dt + dt_bias)
+
+        h_t = exp(d_t A) h_{t-1} + d_t x_t B_t
+        y_t = (C_t . h_t + D x_t) z_t sigmoid(z_t)
+
+    x, dt, z (B, S, D) and B, C (B, S, N), all bfloat16 or all float32,
+    contiguous or a run of columns of a wider tensor, N 16, 32 or 64, z or None
+    (no gate); A (D, N), D and dt_bias (D) or None (zeros), h0 (B, D, N) or None
+    (zero state), float32.  Returns (y, h): y in x's dtype, h (B, D, N) float32,
+    None when return_final_state is False.  A token with dt = -inf leaves the
+    state as it is, so rows of padding need that and finite x and B."""
+    torch = _torch()
+    dev = _gpu_input(x, 3, "(B, S, D)")
+    nb, S, ch, N, (desc, need, _) = _scan_inputs("mlstm_scan_fw", x, dt, A, B, C, D, z, dt_bias, h0)[1:]
+    _check_on(dev, "y", out, (nb, S, ch), x.dtype)
+    workspace, ws_bytes = _bytes_of(need, workspace, dev)
+    y = torch.empty((nb, S, ch), dtype=x.dtype, device=dev) if out is None else out
+    h = torch.empty((nb, ch, N), dtype=torch.float32, device=dev) if return_final_state else None
+    _call("mlstm_scan_fw", dev, desc, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
+          _ptr(h0), _ptr(y), _ptr(h), _ptr(workspace), ws_bytes)
+    return y, h
+
+
+def selective_scan_bw(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, h0=None, dh=None, *, state_grads: bool = False,
+                      workspace=None):
+    """Backward pass of selective_scan_fw on the GPU (mlstm_scan_bw): the
+    gradients of sum(dy * y) + sum(dh * h).  dy has y's shape and x's dtype, dh
+    (B, D, N) float32 or None.  Returns a dict with dx, ddt, dB, dC and, with z,
+    dz in x's dtype, dA, dD and dbias in float32 and, with state_grads, dh0.  The
+    workspace, scan_bw_workspace_bytes of the descriptor (a float32 state for
+    every eight tokens, and more), is allocated here unless it is given."""
+    torch = _torch()
+    dev = _gpu_input(x, 3, "(B, S, D)")
+    nb, S, ch, N, (desc, _, need) = _scan_inputs("mlstm_scan_bw", x, dt, A, B, C, D, z, dt_bias, h0)[1:]
+    _check_on(dev, "dy", dy, (nb, S, ch), x.dtype)
+    _check_on(dev, "dh", dh, (nb, ch, N), torch.float32)
+    workspace, ws_bytes = _bytes_of(need, workspace, dev)
+
+    def rows(n):
+        return torch.empty((nb, S, n), dtype=x.dtype, device=dev)
+
+    def floats(*shape):
+        return torch.empty(shape, dtype=torch.float32, device=dev)
+
+    g = dict(dx=rows(ch), ddt=rows(ch), dA=floats(ch, N), dB=rows(N), dC=rows(N), dD=floats(ch), dbias=floats(ch))
+    if z is not None:
+        g["dz"] = rows(ch)
+    if state_grads:
+        g["dh0"] = floats(nb, ch, N)
+    _call("mlstm_scan_bw", dev, desc, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
+          _ptr(h0), _ptr(dy), _ptr(dh), _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]),
+          _ptr(g["dD"]), _ptr(g.get("dz")), _ptr(g["dbias"]), _ptr(g.get("dh0")), _ptr(workspace), ws_bytes)
+    return g
+
+
+def selective_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, h=None, *, h_out=None):
+    """One token of selective_scan_fw on the GPU (mlstm_scan_step): x, dt, z
+    (B, D), B, C (B, N), h (B, D, N) float32 or None (zero state).  Returns
+    (y, h'); h_out may be h itself (updated in place)."""
+    torch = _torch()
+    dev = _gpu_input(x, 2, "(B, D)")
+    nb, _, ch, N, (desc, _, _) = _scan_inputs("mlstm_scan_step", x, dt, A, B, C, D, z, dt_bias, h)[1:]
+    _check_on(dev, "h_out", h_out, (nb, ch, N), torch.float32)
+    y = torch.empty((nb, ch), dtype=x.dtype, device=dev)
+    if h_out is None:
+        h_out = torch.empty((nb, ch, N), dtype=torch.float32, device=dev)
+    _call("mlstm_scan_step", dev, desc, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
+          _ptr(h), _ptr(y), _ptr(h_out))
+    return y, h_out
+
+
+def _scan_function():
+    """The autograd function of selective_scan."""
+    torch = _torch()
+    if "scan" not in _functions:
+        class SelectiveScan(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, dt, A, B, C, D, z, dt_bias, h0, final_state):
+                y, h = selective_scan_fw(x, dt, A, B, C, D, z, dt_bias, h0, return_final_state=final_state)
+                ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, h0)
+                ctx.set_materialize_grads(False)
+                return (y, h) if final_state else y
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy, dh=None):
+                x, dt, A, B, C, D, z, dt_bias, h0 = ctx.saved_tensors
+                if dy is None and dh is None:
+                    return (None,) * 10
+                dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _readable(dy)
+                g = selective_scan_bw(x, dt, A, B, C, dy, D, z, dt_bias, h0, None if dh is None else _readable(dh),
+                                      state_grads=ctx.needs_input_grad[8])
+                return (g["dx"], g["ddt"], g["dA"], g["dB"], g["dC"], None if D is None else g["dD"], g.get("dz"),
+                        None if dt_bias is None else g["dbias"], g.get("dh0"), None)
+
+        _functions["scan"] = SelectiveScan
+    return _functions["scan"]
+
+
+def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, return_final_state: bool = False):
+    """selective_scan_fw as a torch autograd function (gradients for every
+    tensor by mlstm_scan_bw).  Returns y, or (y, h) with return_final_state;
+    gradients flow in through both.  A pass may be captured into a graph as long
+    as no eager graph of the same leaves is alive meanwhile."""
+    return _scan_function().apply(x, dt, A, B, C, D, z, dt_bias, h0, return_final_state)
+
+
+# ---------------------------------------------------------------------------
+# dropout
+
+def make_dropout_desc(n, p, seed=0, offset=0, *, dtype=MLSTM_F32) -> DropoutDesc:
+    d = DropoutDesc()
+    d.n, d.p, d.seed, d.offset, d.dtype = n, p, _word64(seed, "seed"), _word64(offset, "offset"), dtype
+    return d
+
+
+def dropout_validate(desc: DropoutDesc) -> int:
+    return lib().mlstm_dropout_validate(ctypes.byref(desc))
+
+
+def _word64(value, name) -> int:
+    """An integer of 64 bits, signed or not, as the signed one."""
+    value = int(value)
+    if not -2 ** 63 <= value < 2 ** 64:
+        raise ValueError(f"{name} must have 64 bits, got {value}")
+    return value - 2 ** 64 if value >= 2 ** 63 else value
+
+
+def dropout_fw(x, p: float, seed, offset: int = 0, *, residual=None, out=None):
+    """Dropout with a mask that is never stored, on the GPU (mlstm_dropout):
+    every value of x is dropped with probability p, as the generator with this
+    seed and offset says, or scaled by 1 / (1 - p); residual is added.
+
+    x, residual: contiguous, bfloat16 or float32.  seed, offset: integers of 64
+    bits, or seed an int64 tensor of two values (seed, offset) on x's device,
+    read when the kernel runs (a captured call takes what it holds at each
+    replay).  Which values are dropped depends on p, seed, offset and a value's
+    place in x alone: calls that should differ need another offset.  out may be x
+    or residual itself."""
+    torch = _torch()
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    dev = x.device
+    _check_on(dev, "x", x, x.shape, x.dtype)
+    _check_on(dev, "residual", residual, x.shape, x.dtype)
+    _check_on(dev, "y", out, x.shape, x.dtype)
+    seed_dev = None
+    if isinstance(seed, torch.Tensor) and seed.is_cuda:
+        _check_on(dev, "seed", seed, (2,), torch.int64)
+        if offset:
+            raise ValueError("offset is the second value of a seed tensor")
+        seed, seed_dev = 0, seed
+    desc = make_dropout_desc(x.numel(), float(p), seed, offset, dtype=_out_code(x.dtype, "x"))
+    st = dropout_validate(desc)
+    if st:
+        raise MlstmError(st, "mlstm_dropout")
+    y = torch.empty_like(x) if out is None else out
+    _call("mlstm_dropout", dev, ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(seed_dev), _ptr(y))
+    return y
+
+
+def _dropout_function():
+    """The autograd function of dropout."""
+    torch = _torch()
+    if "dropout" not in _functions:
+        class Dropout(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, p, seed, offset, residual):
+                ctx.save_for_backward(seed if isinstance(seed, torch.Tensor) else None)
+                ctx.p, ctx.seed, ctx.offset = p, None if isinstance(seed, torch.Tensor) else seed, offset
+                return dropout_fw(x, p, seed, offset, residual=residual)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy):
+                seed, = ctx.saved_tensors
+                dx = None
+                if ctx.needs_input_grad[0]:
+                    dx = dropout_fw(dy.contiguous(), ctx.p, ctx.seed if seed is None else seed, ctx.offset)
+                return dx, None, None, None, dy if ctx.needs_input_grad[4] else None
+
+        _functions["dropout"] = Dropout
+    return _functions["dropout"]
+
+
+def dropout(x, p: float, seed, offset: int = 0, *, residual=None):
+    """dropout_fw as a torch autograd function: the gradient for x forms the
+    mask again, the one for residual is the incoming one."""
+    return _dropout_function().apply(x, float(p), seed, offset, residual)

@@ -333,4 +333,90 @@ int head_norm_blocks(int B, int NH, int S, int D);
 hipError_t launch_head_norm(const HeadNormParams& p, hipStream_t stream);
 hipError_t launch_head_norm_back(const HeadNormParams& p, hipStream_t stream);
 
+// A view of (B, S, columns): strides in elements from a sequence to the next
+// and from a token to the next.
+struct View {
+  const void* p;
+  int64_t batch, token;
+};
+
+// Short causal convolution (conv_kernel.hip).
+struct ConvParams {
+  View x;
+  const float* weight;     // (D, K)
+  const float* bias;       // (D), may be null
+  const void* state;       // (B, K - 1, D), may be null
+  void* y;                 // (B, S, D)
+  void* state_out;         // (B, K - 1, D), may be null; step: may equal state
+  const void* dy;          // (B, S, D)
+  const void* dstate_out;  // (B, K - 1, D), may be null
+  void* dx;                // (B, S, D)
+  void* dstate;            // (B, K - 1, D), may be null
+  float* dweight;          // (D, K), may be null
+  float* dbias;            // (D), may be null
+  float* partial;          // (runs, K + 1, D), null when neither sum is wanted
+  int B, S, D, K;
+  int runs, run;           // backward: runs of `run` rows of xe a sequence, `runs` in all
+  int bf16, silu;
+};
+// Rows a run of the backward pass has, and runs of all sequences together.
+void conv_runs(int B, int S, int D, int K, int* run, int* runs);
+hipError_t launch_conv(const ConvParams& p, hipStream_t stream);
+hipError_t launch_conv_back(const ConvParams& p, hipStream_t stream);
+hipError_t launch_conv_step(const ConvParams& p, hipStream_t stream);
+
+// Selective scan (scan_kernel.hip, scan_back_kernel.hip, scan_step_kernel.hip).
+constexpr int kScanTile = 16;      // tokens of a tile of the forward walk
+constexpr int kScanBlock = 8;      // tokens between two kept states of the backward pass
+constexpr int kScanChannels = 64;  // channels of a workgroup of the forward walk
+// Channels of a workgroup of the backward pass.
+__host__ __device__ constexpr int scan_back_channels(int N) { return 2048 / N; }
+struct ScanParams {
+  View x, dt, z, Bm, Cm;   // z.p may be null
+  const float* A;          // (D, N)
+  const float* Dskip;      // (D), may be null
+  const float* bias;       // (D), may be null
+  const float* h0;         // (B, D, N), may be null
+  void* y;
+  float* h_out;            // may be null
+  float* bc;               // (B, rows, 2, N): Bm, Cm in float32, zeros behind the sequence
+  float* ends;             // (B, chunks, D, N): what a chunk leaves of a zero state
+  float* grads;            // (B, chunks, D, N): backward, the gradient a chunk hands on by itself
+  float* sums;             // (B, chunks, D): sum of d over a chunk
+  float* kept;             // (B, rows / 8, D, N): backward, the state in front of every eight tokens
+  const void* dy;
+  const float* dh_out;     // may be null
+  void *dx, *ddt, *dBm, *dCm, *dz;
+  float *dA, *dDskip, *dbias, *dh0;
+  float* part_bc;          // (ceil(D / scan_back_channels), B, S, 2, N)
+  float* part_a;           // (B chunks, D, N)
+  float* part_d;           // (B chunks, 2, D)
+  int B, S, D, N;
+  int rows;                // S rounded up to a tile
+  int chunks, chunk;       // chunks of `chunk` tokens (a multiple of a tile)
+  int bf16;
+};
+// Chunks of the sequence that are walked side by side.
+int scan_chunks(int B, int S, int D, int N, bool back);
+hipError_t launch_scan(const ScanParams& p, hipStream_t stream);
+hipError_t launch_scan_back(const ScanParams& p, hipStream_t stream);
+hipError_t launch_scan_step(const ScanParams& p, hipStream_t stream);
+// What the backward pass takes of the forward walk: Bm and Cm in float32, the
+// chunks' ends and gradients, the kept states.
+hipError_t launch_scan_states(const ScanParams& p, hipStream_t stream);
+
+// Dropout (dropout_kernel.hip).
+struct DropoutParams {
+  const void* x;
+  const void* residual;     // may be null
+  const int64_t* seed_dev;  // may be null
+  void* y;
+  int64_t n;
+  uint64_t seed, offset;
+  uint32_t limit;           // a word below it drops its value
+  float scale;
+  int bf16;
+};
+hipError_t launch_dropout(const DropoutParams& p, hipStream_t stream);
+
 }  // namespace mlstm

@@ -1,0 +1,391 @@
+// Selective scan, gradients, gfx950.  With dr = dy z sigmoid(z) and the state
+// gradient g walked from the last token to the first:
+//   g_t = C_t dr_t + a_{t+1} g_{t+1},   a = exp(d A),   w_t = a_t g_t h_{t-1}
+//   dC_t = sum_c dr h_t,   dB_t = sum_c u g_t,   s = sum_n g B
+//   dx = d s + D dr,   d_d = x s + sum_n A w,   ddt = d_d sigmoid(dt + bias)
+//   dz = dy r (d silu / dz),   dA = sum_t d w,   dD = sum dr x
+//
+// The forward walk has left the state in front of every eight tokens.  A block
+// of eight tokens forms its states and decays again and keeps them in registers
+// while it walks back.  A wave has 32 channels and sixteen states of each: lane l
+// holds channels l % 16 and l % 16 + 16 and four states 4 (l / 16) ..., so that
+// the sums over states run over four lanes and those over channels over sixteen,
+// after two or four values in the lane.  N / 16 waves have the same channels and
+// add their sums over states in LDS; waves with the same states add their parts
+// of dB and dC there and leave one part for the workgroup's 2048 / N channels.
+// Kernels behind this one add those, and the parts of dA, dD and dbias that each
+// chunk of tokens leaves, in a fixed order.
+#include "scan_common.h"
+
+namespace mlstm {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves, T = kScanBlock;
+
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Lanes 0..31: a summed over lanes l and l + 32; lanes 32..63: b.
+__device__ __forceinline__ float halves(float a, float b) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+// Even rows of sixteen lanes: a summed over the row and the next; odd rows: b.
+__device__ __forceinline__ float rows(float a, float b) {
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+// Eight values summed over sixteen lanes: lane l of a row gets value l % 16 / 2.
+__device__ __forceinline__ float row_sums(const float (&v)[8], int l) {
+  float a[4], b[2];
+  const bool b3 = l & 8, b2 = l & 4, b1 = l & 2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = (b3 ? v[i + 4] : v[i]) + moved<0x128>(b3 ? v[i] : v[i + 4]);  // rotated by eight
+#pragma unroll
+  for (int i = 0; i < 2; ++i) b[i] = (b2 ? a[i + 2] : a[i]) + moved<0x141>(b2 ? a[i] : a[i + 2]);  // half row mirrored
+  const float c = (b1 ? b[1] : b[0]) + moved<0x4E>(b1 ? b[0] : b[1]);                              // lane ^ 2
+  return c + moved<0xB1>(c);                                                                       // lane ^ 1
+}
+
+template <typename IO>
+__device__ __forceinline__ float at(const View& v, int b, int t, int d) {
+  return scan_load(static_cast<const IO*>(v.p) + (size_t)b * v.batch + (size_t)t * v.token + d);
+}
+
+template <typename IO, int N, bool GATED>
+__global__ __launch_bounds__(kThreads) void scan_back_kernel(const ScanParams p) {
+  constexpr int NT = N / 16;                        // waves that share channels, sixteen states each
+  constexpr int GROUPS = kWaves / NT, CH = 32 * GROUPS;
+  constexpr int R = 4 / NT;                         // items of a lane
+  constexpr int PER = 2 * N * T / kThreads;         // values of B and C of a block for a thread
+  __shared__ float2 s_d[GROUPS][T][16], s_u[GROUPS][T][16], s_dr[GROUPS][T][16];  // both channels of a lane
+  __shared__ float4 s_bc[2][T][2][N / 4];
+  __shared__ float s_part[2][GROUPS][T][2 * N];
+  __shared__ float s_red[kWaves][T][4][16];
+  __shared__ float s_r[GATED ? kWaves : 1][T / 2][4][16];
+
+  const int nd = (p.D + CH - 1) / CH;
+  const int db = blockIdx.x % nd, bc = blockIdx.x / nd, c = bc % p.chunks, b = bc / p.chunks;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nt = w % NT, grp = w / NT;
+  const int dl = lane & 15, g = lane >> 4, n0 = 16 * nt + 4 * g;
+  const int d0 = db * CH + 32 * grp + dl;
+  const bool in[2] = {d0 < p.D, d0 + 16 < p.D};
+  const int dch[2] = {in[0] ? d0 : p.D - 1, in[1] ? d0 + 16 : p.D - 1};
+  const int t0 = c * p.chunk, t1 = min(t0 + p.chunk, p.S);
+  const int first = t0 / T, last = (t1 + T - 1) / T;  // blocks
+
+  float bias[2], skip[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    bias[k] = p.bias ? p.bias[dch[k]] : 0.0f;
+    skip[k] = p.Dskip ? p.Dskip[dch[k]] : 0.0f;
+  }
+  // i = 4 (channel) + state of four
+  float A2[8], ag[8], dA[8] = {}, dA2[8] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    A2[i] = kLog2e * p.A[(size_t)dch[i / 4] * N + n0 + i % 4];
+    ag[i] = p.dh_out && in[i / 4] ? p.dh_out[((size_t)b * p.D + dch[i / 4]) * N + n0 + i % 4] : 0.0f;
+  }
+  // the state gradient behind this chunk: the chunks behind it, last to first
+  for (int k = p.chunks - 1; k > c; --k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const size_t at = ((size_t)b * p.chunks + k) * p.D + dch[i / 4];
+      ag[i] = fmaf(exp2_fast(p.sums[at] * A2[i]), ag[i], p.grads[at * N + n0 + i % 4]);
+    }
+
+  // item r of a lane: token and channel of the block
+  int tok[R], ch[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    tok[r] = 2 * g + (nt * R + r) / 2;
+    ch[r] = (nt * R + r) % 2;
+  }
+  float rx[R], rdt[R], rdy[R], rz[R], rbc[PER];
+  auto fetch = [&](int blk) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int t = blk * T + tok[r], d = ch[r] ? dch[1] : dch[0];
+      const bool ok = (ch[r] ? in[1] : in[0]) && t < t1;
+      rx[r] = ok ? at<IO>(p.x, b, t, d) : 0.0f;
+      rdt[r] = ok ? at<IO>(p.dt, b, t, d) : -__builtin_inff();
+      rdy[r] = ok ? scan_load(static_cast<const IO*>(p.dy) + ((size_t)b * p.S + t) * p.D + d) : 0.0f;
+      rz[r] = GATED && ok ? at<IO>(p.z, b, t, d) : 0.0f;
+    }
+    const float* from = p.bc + ((size_t)b * p.rows + blk * T) * 2 * N;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) rbc[i] = from[tid + i * kThreads];
+  };
+  float rh[8];
+  auto fetch_state = [&](int blk) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (in[k]) v = *reinterpret_cast<const float4*>(p.kept + (((size_t)b * (p.rows / T) + blk) * p.D + dch[k]) * N + n0);
+      rh[4 * k] = v.x;
+      rh[4 * k + 1] = v.y;
+      rh[4 * k + 2] = v.z;
+      rh[4 * k + 3] = v.w;
+    }
+  };
+  auto add_parts = [&](int buf, int blk) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = tid + i * kThreads, t = e / (2 * N), col = e % (2 * N);
+      float s = s_part[buf][0][t][col];
+#pragma unroll
+      for (int k = 1; k < GROUPS; ++k) s += s_part[buf][k][t][col];
+      if (blk * T + t < t1) p.part_bc[(((size_t)db * p.B + b) * p.S + blk * T + t) * 2 * N + col] = s;
+    }
+  };
+  // the waves of a group have written what they read of each other
+  auto group_sync = [] {
+    if constexpr (NT > 1)
+      __syncthreads();
+    else
+      wave_sync();
+  };
+
+  float dskip[2] = {}, dbias[2] = {}, dskip2[2] = {}, dbias2[2] = {};
+  if (first < last) {
+    fetch(last - 1);
+    fetch_state(last - 1);
+  }
+  int buf = 0;
+  for (int blk = last - 1; blk >= first; --blk, buf ^= 1) {
+    float x[R], sg[R], dlt[R], dr[R], dy[R], z[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float pre = rdt[r] + (ch[r] ? bias[1] : bias[0]);
+      x[r] = rx[r];
+      dy[r] = rdy[r];
+      z[r] = rz[r];
+      dlt[r] = softplus(pre);
+      sg[r] = scan_sigmoid(pre);
+      dr[r] = GATED ? dy[r] * z[r] * scan_sigmoid(z[r]) : dy[r];
+      reinterpret_cast<float*>(&s_d[grp][tok[r]][dl])[ch[r]] = dlt[r];
+      reinterpret_cast<float*>(&s_u[grp][tok[r]][dl])[ch[r]] = dlt[r] * x[r];
+      reinterpret_cast<float*>(&s_dr[grp][tok[r]][dl])[ch[r]] = dr[r];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) reinterpret_cast<float*>(s_bc[buf])[tid + i * kThreads] = rbc[i];
+    __syncthreads();
+    if (blk < last - 1) add_parts(buf ^ 1, blk + 1);
+    if (blk > first) fetch(blk - 1);
+
+    float h0[8], a[T][8], h[T][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h0[i] = rh[i];
+    if (blk > first) fetch_state(blk - 1);
+    float y[2][2];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const float2 d2 = s_d[grp][t][dl], u2 = s_u[grp][t][dl];
+      const float4 B4 = s_bc[buf][t][0][4 * nt + g];
+      const float B[4] = {B4.x, B4.y, B4.z, B4.w}, de[2] = {d2.x, d2.y}, u[2] = {u2.x, u2.y};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[t][i] = exp2_fast(de[i / 4] * A2[i]);
+        h[t][i] = fmaf(a[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], u[i / 4] * B[i % 4]);
+      }
+      if (GATED) {
+        const float4 C4 = s_bc[buf][t][1][4 * nt + g];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          y[t % 2][k] = C4.x * h[t][4 * k] + C4.y * h[t][4 * k + 1] + C4.z * h[t][4 * k + 2] + C4.w * h[t][4 * k + 3];
+        if (t % 2) s_r[w][t / 2][g][dl] = rows(halves(y[0][0], y[0][1]), halves(y[1][0], y[1][1]));
+      }
+    }
+    float da[8] = {};
+#pragma unroll
+    for (int t = T - 1; t >= 0; --t) {
+      const float4 B4 = s_bc[buf][t][0][4 * nt + g], C4 = s_bc[buf][t][1][4 * nt + g];
+      const float2 d2 = s_d[grp][t][dl], u2 = s_u[grp][t][dl], r2 = s_dr[grp][t][dl];
+      const float B[4] = {B4.x, B4.y, B4.z, B4.w}, C[4] = {C4.x, C4.y, C4.z, C4.w};
+      const float de[2] = {d2.x, d2.y}, u[2] = {u2.x, u2.y}, r[2] = {r2.x, r2.y};
+      float v[8], s[2] = {}, wa[2] = {};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = i / 4, n = i % 4;
+        const float gi = fmaf(C[n], r[k], ag[i]);
+        v[n] = k ? fmaf(gi, u[k], v[n]) : gi * u[k];
+        v[4 + n] = k ? fmaf(h[t][i], r[k], v[4 + n]) : h[t][i] * r[k];
+        s[k] = fmaf(gi, B[n], s[k]);
+        ag[i] = a[t][i] * gi;
+        const float wi = ag[i] * (t ? h[t ? t - 1 : 0][i] : h0[i]);
+        da[i] = fmaf(de[k], wi, da[i]);
+        wa[k] = fmaf(A2[i], wi, wa[k]);
+      }
+      const float v1 = row_sums(v, lane);
+      if (lane % 2 == 0) s_part[buf][grp][t][(dl / 8) * N + n0 + dl / 2 % 4] = v1;
+      s_red[w][t][g][dl] = rows(halves(s[0], s[1]), halves(wa[0], wa[1]));
+    }
+    // long sums in three steps: eight tokens, 32 blocks, all of them
+    const bool flush = blk % 32 == 0 || blk == first;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dA2[i] += da[i];
+      if (flush) {
+        dA[i] += dA2[i];
+        dA2[i] = 0.0f;
+      }
+    }
+    group_sync();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int t = blk * T + tok[r], q = tok[r];
+      const bool k = ch[r];
+      float s = 0.0f, wa = 0.0f, y1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        s += s_red[grp * NT + j][q][2 * k][dl];
+        wa += s_red[grp * NT + j][q][2 * k + 1][dl];
+        if (GATED) y1 += s_r[grp * NT + j][q / 2][q % 2 + 2 * k][dl];
+      }
+      const float sk = k ? skip[1] : skip[0];
+      const float dx = fmaf(dlt[r], s, sk * dr[r]), ddt = fmaf(x[r], s, kLn2 * wa) * sg[r], dd = dr[r] * x[r];
+      dskip2[0] += k ? 0.0f : dd;
+      dskip2[1] += k ? dd : 0.0f;
+      dbias2[0] += k ? 0.0f : ddt;
+      dbias2[1] += k ? ddt : 0.0f;
+      if ((k ? in[1] : in[0]) && t < t1) {
+        const size_t o = ((size_t)b * p.S + t) * p.D + (k ? dch[1] : dch[0]);
+        scan_store(static_cast<IO*>(p.dx) + o, dx);
+        scan_store(static_cast<IO*>(p.ddt) + o, ddt);
+        if (GATED) {
+          const float sz = scan_sigmoid(z[r]);
+          scan_store(static_cast<IO*>(p.dz) + o, dy[r] * fmaf(sk, x[r], y1) * sz * (1.0f + z[r] * (1.0f - sz)));
+        }
+      }
+    }
+    if (flush) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        dskip[k] += dskip2[k];
+        dbias[k] += dbias2[k];
+        dskip2[k] = dbias2[k] = 0.0f;
+      }
+    }
+    group_sync();
+  }
+  __syncthreads();
+  if (first < last) add_parts(buf ^ 1, first);
+
+  const size_t part = (size_t)b * p.chunks + c;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (in[k]) {
+      *reinterpret_cast<float4*>(p.part_a + (part * p.D + dch[k]) * N + n0) =
+          make_float4(dA[4 * k], dA[4 * k + 1], dA[4 * k + 2], dA[4 * k + 3]);
+      if (c == 0 && p.dh0)
+        *reinterpret_cast<float4*>(p.dh0 + ((size_t)b * p.D + dch[k]) * N + n0) =
+            make_float4(ag[4 * k], ag[4 * k + 1], ag[4 * k + 2], ag[4 * k + 3]);
+    }
+  // dD and dbias of a channel: over the lanes that have it, then over the waves of the group
+  s_red[w][0][g][dl] = rows(halves(dskip[0], dskip[1]), halves(dbias[0], dbias[1]));
+  group_sync();
+  if (nt == 0) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) s += s_red[w + j][0][g][dl];
+    const int k = g >> 1;
+    if (k ? in[1] : in[0]) p.part_d[(part * 2 + (g & 1)) * p.D + (k ? dch[1] : dch[0])] = s;
+  }
+}
+
+// dBm, dCm: the parts of the channel groups, in order.
+template <typename IO>
+__global__ __launch_bounds__(kThreads) void scan_back_columns_kernel(const ScanParams p) {
+  const int64_t n = (int64_t)p.B * p.S * 2 * p.N;
+  const int groups = (p.D + scan_back_channels(p.N) - 1) / scan_back_channels(p.N);
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+    float s = 0.0f;
+    for (int k = 0; k < groups; ++k) s += p.part_bc[k * n + i];
+    const int64_t row = i / (2 * p.N);
+    const int col = (int)(i - row * 2 * p.N);
+    IO* out = static_cast<IO*>(col < p.N ? p.dBm : p.dCm);
+    scan_store(out + row * p.N + (col < p.N ? col : col - p.N), s);
+  }
+}
+
+// dA, dD and dbias: the parts of the chunks, in order.
+__global__ __launch_bounds__(kThreads) void scan_back_sums_kernel(const ScanParams p) {
+  const int64_t na = (int64_t)p.D * p.N, n = na + 2 * p.D;
+  const int parts = p.S > 0 ? p.B * p.chunks : 0;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+    float s = 0.0f;
+    const float* from = i < na ? p.part_a + i : p.part_d + (i - na);
+    const int64_t step = i < na ? na : 2 * p.D;
+    for (int k = 0; k < parts; ++k) s += from[k * step];
+    if (i < na)
+      p.dA[i] = s;
+    else if (i < na + p.D) {
+      if (p.dDskip) p.dDskip[i - na] = s;
+    } else if (p.dbias) {
+      p.dbias[i - na - p.D] = s;
+    }
+  }
+}
+
+// No tokens: the state's gradient passes through.
+__global__ __launch_bounds__(kThreads) void scan_back_copy_kernel(const ScanParams p) {
+  const int64_t n = (int64_t)p.B * p.D * p.N;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads)
+    p.dh0[i] = p.dh_out ? p.dh_out[i] : 0.0f;
+}
+
+unsigned groups_for(int64_t threads) {
+  const int64_t g = (threads + kThreads - 1) / kThreads;
+  return (unsigned)(g < 1 ? 1 : g < (1 << 20) ? g : 1 << 20);
+}
+
+template <typename IO, int N>
+hipError_t launch_gated(const ScanParams& p, hipStream_t stream) {
+  const unsigned nd = (unsigned)((p.D + scan_back_channels(N) - 1) / scan_back_channels(N));
+  const dim3 grid(nd * (unsigned)p.chunks * (unsigned)p.B);
+  if (p.z.p)
+    hipLaunchKernelGGL((scan_back_kernel<IO, N, true>), grid, dim3(kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((scan_back_kernel<IO, N, false>), grid, dim3(kThreads), 0, stream, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((scan_back_columns_kernel<IO>), dim3(groups_for((int64_t)p.B * p.S * 2 * N)), dim3(kThreads), 0,
+                     stream, p);
+  return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t launch_states(const ScanParams& p, hipStream_t stream) {
+  switch (p.N) {
+    case 16: return launch_gated<IO, 16>(p, stream);
+    case 32: return launch_gated<IO, 32>(p, stream);
+    case 64: return launch_gated<IO, 64>(p, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_scan_back(const ScanParams& p, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (p.S > 0) {
+    e = launch_scan_states(p, stream);
+    if (e == hipSuccess) e = p.bf16 ? launch_states<bf16_t>(p, stream) : launch_states<float>(p, stream);
+  } else if (p.dh0) {
+    hipLaunchKernelGGL(scan_back_copy_kernel, dim3(groups_for((int64_t)p.B * p.D * p.N)), dim3(kThreads), 0, stream, p);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(scan_back_sums_kernel, dim3(groups_for((int64_t)p.D * (p.N + 2))), dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace mlstm
