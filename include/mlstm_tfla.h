@@ -684,7 +684,7 @@ int mlstm_head_norm_bw(const mlstm_head_norm_desc_t* desc,
  * projection's output): its channels are adjacent, and the descriptor has its
  * strides in elements, from one sequence to the next and from one token to the
  * next; 0 stands for the stride of a contiguous tensor.  The token's stride is
- * at least the number of columns (tokens do not overlap) and below 2^26.  Such
+ * at least the number of columns (tokens do not overlap) and below 2^25.  Such
  * inputs need the alignment of one element only.  Everything else is contiguous.
  *
  * Short causal convolution, every channel by itself, K taps:
@@ -698,7 +698,7 @@ int mlstm_head_norm_bw(const mlstm_head_norm_desc_t* desc,
 typedef struct {
   int32_t B, S, D;     /* B, D >= 1, S >= 0; B * (S + 3) * D below 2^40,
                           B * (S + 3) below 2^32, S below 2^30, D below
-                          2^26, B below 2^16                                  */
+                          2^22, B below 2^16                                  */
   int32_t K;           /* taps: 2, 3 or 4                                     */
   int32_t dtype;       /* mlstm_dtype_t of x, y, the states, and gradients    */
   int32_t silu;        /* 1: y = p sigmoid(p); 0: y = p                       */
@@ -753,7 +753,7 @@ int mlstm_conv_step(const mlstm_conv_desc_t* desc,
  * it too); a non-finite Bm or Cm reaches every channel. */
 typedef struct {
   int32_t B, S, D;     /* B, D >= 1, S >= 0; B * S * D below 2^40, S below
-                          2^30, D below 2^26, B * ceil(D / 64) below 2^20     */
+                          2^30, D below 2^22, B * ceil(D / 64) below 2^20     */
   int32_t N;           /* states a channel: 16, 32 or 64                      */
   int32_t dtype;       /* mlstm_dtype_t of x, dt, Bm, Cm, z, y and gradients  */
   int32_t reserved0;   /* must be zero                                        */

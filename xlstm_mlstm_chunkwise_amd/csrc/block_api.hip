@@ -39,13 +39,13 @@ mlstm::View view(const void* p, const int64_t (&strides)[2], int64_t S, int64_t 
 // A token's columns lie side by side and tokens do not overlap; a token's
 // stride keeps offsets over a few tokens in 32 bits, a batch's the others in 62.
 bool bad_strides(const int64_t (&s)[2], int64_t B, int64_t columns) {
-  return s[0] < 0 || s[0] > ((int64_t)1 << 59) / B || (s[1] && (s[1] < columns || s[1] >= (1 << 26)));
+  return s[0] < 0 || s[0] > ((int64_t)1 << 59) / B || (s[1] && (s[1] < columns || s[1] >= (1 << 25)));
 }
 
 // B, S and D as the descriptors' comments have them.
 bool bad_shape(int64_t B, int64_t S, int64_t D, int64_t more) {
   return B < 1 || D < 1 || S < 0 || S >= (1 << 30) || B * (S + more) >= ((int64_t)1 << 40) ||
-         (B * (S + more)) * (D < (1 << 23) ? D : (int64_t)1 << 23) >= ((int64_t)1 << 40) || D >= (1 << 26);
+         (B * (S + more)) * (D < (1 << 23) ? D : (int64_t)1 << 23) >= ((int64_t)1 << 40) || D >= (1 << 22);
 }
 
 int validate(const mlstm_conv_desc_t* d) {
@@ -116,10 +116,7 @@ mlstm::ScanParams params(const mlstm_scan_desc_t* d, const void* x, const void* 
 // Cuts the sequence, places the workspace (none: sizes only) and returns its bytes.
 size_t place(mlstm::ScanParams& p, bool back, void* workspace) {
   p.rows = (p.S + mlstm::kScanTile - 1) / mlstm::kScanTile * mlstm::kScanTile;
-  p.chunks = mlstm::scan_chunks(p.B, p.S, p.D, p.N, back);
-  const int tiles = p.rows / mlstm::kScanTile;
-  p.chunk = (tiles + p.chunks - 1) / p.chunks * mlstm::kScanTile;
-  if (p.chunk) p.chunks = (p.S + p.chunk - 1) / p.chunk;  // every chunk has tokens
+  mlstm::scan_cut(p, back);
   size_t off = 0;
   char* ws = static_cast<char*>(workspace);
   auto take = [&](size_t floats) {
@@ -127,20 +124,23 @@ size_t place(mlstm::ScanParams& p, bool back, void* workspace) {
     off += round_up(floats * sizeof(float));
     return at;
   };
-  const size_t B = p.B, S = p.S, D = p.D, N = p.N, states = B * p.chunks * D;
+  const size_t B = p.B, S = p.S, D = p.D, N = p.N, states = B * p.chunks * D, spans = B * p.spans * D;
   if (!S) return 0;
   p.bc = take(B * p.rows * 2 * N);
   if (p.chunks > 1) {
     p.ends = take(states * N);
     p.sums = take(states);
-    if (back) p.grads = take(states * N);
   }
   if (back) {
     const size_t ch = mlstm::scan_back_channels(p.N);
+    if (p.spans > 1) {
+      p.grads = take(spans * N);
+      p.span_sums = take(spans);
+    }
     p.kept = take(B * (p.rows / mlstm::kScanBlock) * D * N);
     p.part_bc = take((D + ch - 1) / ch * B * S * 2 * N);
-    p.part_a = take(states * N);
-    p.part_d = take(states * 2);
+    p.part_a = take(spans * N);
+    p.part_d = take(spans * 2);
   }
   return off;
 }

@@ -366,6 +366,7 @@ hipError_t launch_conv_back(const ConvParams& p, hipStream_t stream);
 hipError_t launch_conv_step(const ConvParams& p, hipStream_t stream);
 
 // Selective scan (scan_kernel.hip, scan_back_kernel.hip, scan_step_kernel.hip).
+constexpr int kScanWaves = 8;      // waves of a workgroup of the forward walk: parts of a channel's states
 constexpr int kScanTile = 16;      // tokens of a tile of the forward walk
 constexpr int kScanBlock = 8;      // tokens between two kept states of the backward pass
 constexpr int kScanChannels = 64;  // channels of a workgroup of the forward walk
@@ -379,30 +380,43 @@ struct ScanParams {
   const float* h0;         // (B, D, N), may be null
   void* y;
   float* h_out;            // may be null
-  float* bc;               // (B, rows, 2, N): Bm, Cm in float32, zeros behind the sequence
+  float* bc;               // Bm, Cm in float32 (see scan_columns), zeros behind the sequence
   float* ends;             // (B, chunks, D, N): what a chunk leaves of a zero state
-  float* grads;            // (B, chunks, D, N): backward, the gradient a chunk hands on by itself
   float* sums;             // (B, chunks, D): sum of d over a chunk
-  float* kept;             // (B, rows / 8, D, N): backward, the state in front of every eight tokens
+  float* grads;            // (B, spans, D, N): backward, the state gradient a span hands on by itself
+  float* span_sums;        // (B, spans, D): sum of d over a span
+  float* kept;             // (B, rows / 8, N / 2, D, 2): backward, the state in front of every eight tokens
   const void* dy;
   const float* dh_out;     // may be null
   void *dx, *ddt, *dBm, *dCm, *dz;
   float *dA, *dDskip, *dbias, *dh0;
   float* part_bc;          // (ceil(D / scan_back_channels), B, S, 2, N)
-  float* part_a;           // (B chunks, D, N)
-  float* part_d;           // (B chunks, 2, D)
+  float* part_a;           // (B spans, D, N)
+  float* part_d;           // (B spans, 2, D)
   int B, S, D, N;
   int rows;                // S rounded up to a tile
-  int chunks, chunk;       // chunks of `chunk` tokens (a multiple of a tile)
+  int chunks, chunk;       // chunks of `chunk` tokens that the states are walked in (a multiple of a tile)
+  int spans, span;         // spans of `span` tokens that the gradients are walked in; a chunk is whole spans
   int bf16;
 };
-// Chunks of the sequence that are walked side by side.
-int scan_chunks(int B, int S, int D, int N, bool back);
+// Where a value of Bm or Cm lies in bc.  A wave reads the sixteen values of B of
+// 16 kScanWaves / N tokens at once, and those of C: they lie together, for one
+// wave after the other.  e counts the values of tokens from such a group on.
+struct ScanColumn {
+  int token, state, which;  // which: 0 of Bm, 1 of Cm
+};
+__host__ __device__ constexpr ScanColumn scan_column(int e, int N) {
+  const int per = N / kScanWaves, group = 32 * kScanWaves;
+  return {e / group * (16 / per) + e % 16 / per, e % group / 32 * per + e % per, e / 16 % 2};
+}
+// Cuts the sequence into chunks and, for the backward pass, spans that are
+// walked side by side.
+void scan_cut(ScanParams& p, bool back);
 hipError_t launch_scan(const ScanParams& p, hipStream_t stream);
 hipError_t launch_scan_back(const ScanParams& p, hipStream_t stream);
 hipError_t launch_scan_step(const ScanParams& p, hipStream_t stream);
 // What the backward pass takes of the forward walk: Bm and Cm in float32, the
-// chunks' ends and gradients, the kept states.
+// kept states, the spans' gradients and sums.
 hipError_t launch_scan_states(const ScanParams& p, hipStream_t stream);
 
 // Dropout (dropout_kernel.hip).

@@ -14,7 +14,7 @@
 // add their sums over states in LDS; waves with the same states add their parts
 // of dB and dC there and leave one part for the workgroup's 2048 / N channels.
 // Kernels behind this one add those, and the parts of dA, dD and dbias that each
-// chunk of tokens leaves, in a fixed order.
+// span of tokens leaves, in a fixed order.
 #include "scan_common.h"
 
 namespace mlstm {
@@ -53,88 +53,110 @@ __device__ __forceinline__ float row_sums(const float (&v)[8], int l) {
   return c + moved<0xB1>(c);                                                                       // lane ^ 1
 }
 
-template <typename IO>
-__device__ __forceinline__ float at(const View& v, int b, int t, int d) {
-  return scan_load(static_cast<const IO*>(v.p) + (size_t)b * v.batch + (size_t)t * v.token + d);
+// The state gradient behind span `c`: the spans behind it, last to first.
+__device__ __forceinline__ void enter(const ScanParams& p, int b, int c, const int (&d)[2], int n0,
+                                      const float (&A2)[8], float (&ag)[8]) {
+  for (int k = p.spans - 1; k > c; k -= 4) {
+    float sum[4][2];
+    float4_t g[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const size_t at = ((size_t)b * p.spans + max(k - j, c)) * p.D + d[e];
+        sum[j][e] = p.span_sums[at];
+        g[j][e] = *reinterpret_cast<const float4_t*>(p.grads + at * p.N + n0);
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k - j > c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ag[i] = fmaf(decay(sum[j][i / 4], A2[i]), ag[i], g[j][i / 4][i % 4]);
+  }
 }
 
 template <typename IO, int N, bool GATED>
-__global__ __launch_bounds__(kThreads) void scan_back_kernel(const ScanParams p) {
+__global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams p) {
   constexpr int NT = N / 16;                        // waves that share channels, sixteen states each
   constexpr int GROUPS = kWaves / NT, CH = 32 * GROUPS;
-  constexpr int R = 4 / NT;                         // items of a lane
+  constexpr int R = 4 / NT;                         // items of a lane: a token and a channel each
   constexpr int PER = 2 * N * T / kThreads;         // values of B and C of a block for a thread
+  typedef typename Raw<IO>::type raw_t;
   __shared__ float2 s_d[GROUPS][T][16], s_u[GROUPS][T][16], s_dr[GROUPS][T][16];  // both channels of a lane
-  __shared__ float4 s_bc[2][T][2][N / 4];
+  __shared__ float4_t s_bc[2][T][2][N / 4];
   __shared__ float s_part[2][GROUPS][T][2 * N];
   __shared__ float s_red[kWaves][T][4][16];
   __shared__ float s_r[GATED ? kWaves : 1][T / 2][4][16];
+  __shared__ float4_t s_item[R][kThreads];          // x, sigmoid(dt), dy silu'(z), dy silu(z)
+  __shared__ float4_t s_dA[2][kThreads];
 
   const int nd = (p.D + CH - 1) / CH;
-  const int db = blockIdx.x % nd, bc = blockIdx.x / nd, c = bc % p.chunks, b = bc / p.chunks;
+  const int db = blockIdx.x % nd, bc = blockIdx.x / nd, c = bc % p.spans, b = bc / p.spans;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nt = w % NT, grp = w / NT;
   const int dl = lane & 15, g = lane >> 4, n0 = 16 * nt + 4 * g;
   const int d0 = db * CH + 32 * grp + dl;
   const bool in[2] = {d0 < p.D, d0 + 16 < p.D};
   const int dch[2] = {in[0] ? d0 : p.D - 1, in[1] ? d0 + 16 : p.D - 1};
-  const int t0 = c * p.chunk, t1 = min(t0 + p.chunk, p.S);
+  const int t0 = c * p.span, t1 = min(t0 + p.span, p.S);
   const int first = t0 / T, last = (t1 + T - 1) / T;  // blocks
 
-  float bias[2], skip[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    bias[k] = p.bias ? p.bias[dch[k]] : 0.0f;
-    skip[k] = p.Dskip ? p.Dskip[dch[k]] : 0.0f;
-  }
   // i = 4 (channel) + state of four
-  float A2[8], ag[8], dA[8] = {}, dA2[8] = {};
+  float A2[8], ag[8], dA[8] = {};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     A2[i] = kLog2e * p.A[(size_t)dch[i / 4] * N + n0 + i % 4];
     ag[i] = p.dh_out && in[i / 4] ? p.dh_out[((size_t)b * p.D + dch[i / 4]) * N + n0 + i % 4] : 0.0f;
   }
-  // the state gradient behind this chunk: the chunks behind it, last to first
-  for (int k = p.chunks - 1; k > c; --k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const size_t at = ((size_t)b * p.chunks + k) * p.D + dch[i / 4];
-      ag[i] = fmaf(exp2_fast(p.sums[at] * A2[i]), ag[i], p.grads[at * N + n0 + i % 4]);
-    }
+  if (c + 1 < p.spans) enter(p, b, c, dch, n0, A2, ag);
+  s_dA[0][tid] = s_dA[1][tid] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
 
-  // item r of a lane: token and channel of the block
-  int tok[R], ch[R];
+  // Item r of a lane: tokens 2 g and 2 g + 1 of the block with both channels each,
+  // which the NT waves of a group share out.
+  auto odd = [&](int r) { return NT == 1 ? r / 2 : NT == 2 ? nt : nt / 2; };
+  auto ch = [&](int r) { return NT == 4 ? nt % 2 : r % 2; };
+  // Rows 2 g, and by another base 2 g + 1, of a block; the end of the span is the end of the resource.
+  auto offset = [&](int64_t stride, int k) {
+    return in[k] ? (uint32_t)((2 * g * stride + d0 + 16 * k) * (int)sizeof(IO)) : kNowhere;
+  };
+  auto rows_at = [&](const void* base, int64_t batch, int64_t stride, int blk, int odd) {
+    const int t = blk * T + odd, n = __builtin_amdgcn_readfirstlane(min(max(t1 - t, 0), T));
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(base)) + (b * batch + t * stride) * (int64_t)sizeof(IO), 0,
+        n * (int)stride * (int)sizeof(IO), 0x00020000);
+  };
+  uint32_t ox[2], odt[2], oz[2], od[2];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    tok[r] = 2 * g + (nt * R + r) / 2;
-    ch[r] = (nt * R + r) % 2;
+  for (int k = 0; k < 2; ++k) {
+    ox[k] = offset(p.x.token, k);
+    odt[k] = offset(p.dt.token, k);
+    if (GATED) oz[k] = offset(p.z.token, k);
+    od[k] = offset(p.D, k);
   }
-  float rx[R], rdt[R], rdy[R], rz[R], rbc[PER];
+  const int64_t batch = (int64_t)p.S * p.D;
+  raw_t rx[R], rdt[R], rdy[R], rz[R];
+  float rbc[PER];
   auto fetch = [&](int blk) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int t = blk * T + tok[r], d = ch[r] ? dch[1] : dch[0];
-      const bool ok = (ch[r] ? in[1] : in[0]) && t < t1;
-      rx[r] = ok ? at<IO>(p.x, b, t, d) : 0.0f;
-      rdt[r] = ok ? at<IO>(p.dt, b, t, d) : -__builtin_inff();
-      rdy[r] = ok ? scan_load(static_cast<const IO*>(p.dy) + ((size_t)b * p.S + t) * p.D + d) : 0.0f;
-      rz[r] = GATED && ok ? at<IO>(p.z, b, t, d) : 0.0f;
+      const int o = odd(r), k = ch(r);
+      rx[r] = Raw<IO>::load(rows_at(p.x.p, p.x.batch, p.x.token, blk, o), k ? ox[1] : ox[0]);
+      rdt[r] = Raw<IO>::load(rows_at(p.dt.p, p.dt.batch, p.dt.token, blk, o), k ? odt[1] : odt[0]);
+      rdy[r] = Raw<IO>::load(rows_at(p.dy, batch, p.D, blk, o), k ? od[1] : od[0]);
+      if (GATED) rz[r] = Raw<IO>::load(rows_at(p.z.p, p.z.batch, p.z.token, blk, o), k ? oz[1] : oz[0]);
     }
     const float* from = p.bc + ((size_t)b * p.rows + blk * T) * 2 * N;
 #pragma unroll
     for (int i = 0; i < PER; ++i) rbc[i] = from[tid + i * kThreads];
   };
-  float rh[8];
+  float2 rh[4];
   auto fetch_state = [&](int blk) {
+    const float2* from = reinterpret_cast<const float2*>(p.kept) +
+                         (((size_t)b * (p.rows / T) + blk) * (N / 2) + n0 / 2) * p.D;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (in[k]) v = *reinterpret_cast<const float4*>(p.kept + (((size_t)b * (p.rows / T) + blk) * p.D + dch[k]) * N + n0);
-      rh[4 * k] = v.x;
-      rh[4 * k + 1] = v.y;
-      rh[4 * k + 2] = v.z;
-      rh[4 * k + 3] = v.w;
-    }
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) rh[2 * k + j] = from[(size_t)j * p.D + dch[k]];
   };
   auto add_parts = [&](int buf, int blk) {
 #pragma unroll
@@ -153,6 +175,8 @@ __global__ __launch_bounds__(kThreads) void scan_back_kernel(const ScanParams p)
     else
       wave_sync();
   };
+  const float bias[2] = {p.bias ? p.bias[dch[0]] : 0.0f, p.bias ? p.bias[dch[1]] : 0.0f};
+  const float skip[2] = {p.Dskip ? p.Dskip[dch[0]] : 0.0f, p.Dskip ? p.Dskip[dch[1]] : 0.0f};
 
   float dskip[2] = {}, dbias[2] = {}, dskip2[2] = {}, dbias2[2] = {};
   if (first < last) {
@@ -161,110 +185,113 @@ __global__ __launch_bounds__(kThreads) void scan_back_kernel(const ScanParams p)
   }
   int buf = 0;
   for (int blk = last - 1; blk >= first; --blk, buf ^= 1) {
-    float x[R], sg[R], dlt[R], dr[R], dy[R], z[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float pre = rdt[r] + (ch[r] ? bias[1] : bias[0]);
-      x[r] = rx[r];
-      dy[r] = rdy[r];
-      z[r] = rz[r];
-      dlt[r] = softplus(pre);
-      sg[r] = scan_sigmoid(pre);
-      dr[r] = GATED ? dy[r] * z[r] * scan_sigmoid(z[r]) : dy[r];
-      reinterpret_cast<float*>(&s_d[grp][tok[r]][dl])[ch[r]] = dlt[r];
-      reinterpret_cast<float*>(&s_u[grp][tok[r]][dl])[ch[r]] = dlt[r] * x[r];
-      reinterpret_cast<float*>(&s_dr[grp][tok[r]][dl])[ch[r]] = dr[r];
+      const int k = ch(r), q = 2 * g + odd(r);
+      const bool ok = (k ? in[1] : in[0]) && blk * T + q < t1;
+      const float pre = Raw<IO>::value(rdt[r]) + (k ? bias[1] : bias[0]);
+      const float x = Raw<IO>::value(rx[r]), dy = Raw<IO>::value(rdy[r]), dlt = ok ? softplus(pre) : 0.0f;
+      float dr = dy, dz = 0.0f;
+      if (GATED) {
+        const float z = Raw<IO>::value(rz[r]), sz = scan_sigmoid(z);
+        dr = dy * (z * sz);
+        dz = dy * (sz * fmaf(z, 1.0f - sz, 1.0f));
+      }
+      reinterpret_cast<float*>(&s_d[grp][q][dl])[k] = dlt;
+      reinterpret_cast<float*>(&s_u[grp][q][dl])[k] = dlt * x;
+      reinterpret_cast<float*>(&s_dr[grp][q][dl])[k] = dr;
+      s_item[r][tid] = (float4_t){x, scan_sigmoid(pre), dz, dr};
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) reinterpret_cast<float*>(s_bc[buf])[tid + i * kThreads] = rbc[i];
+    for (int i = 0; i < PER; ++i) {
+      const ScanColumn col = scan_column(tid + i * kThreads, N);
+      reinterpret_cast<float*>(s_bc[buf])[(col.token * 2 + col.which) * N + col.state] = rbc[i];
+    }
     __syncthreads();
     if (blk < last - 1) add_parts(buf ^ 1, blk + 1);
     if (blk > first) fetch(blk - 1);
 
     float h0[8], a[T][8], h[T][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h0[i] = rh[i];
+    for (int i = 0; i < 4; ++i) {
+      h0[2 * i] = in[i / 2] ? rh[i].x : 0.0f;
+      h0[2 * i + 1] = in[i / 2] ? rh[i].y : 0.0f;
+    }
     if (blk > first) fetch_state(blk - 1);
-    float y[2][2];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const float2 d2 = s_d[grp][t][dl], u2 = s_u[grp][t][dl];
-      const float4 B4 = s_bc[buf][t][0][4 * nt + g];
-      const float B[4] = {B4.x, B4.y, B4.z, B4.w}, de[2] = {d2.x, d2.y}, u[2] = {u2.x, u2.y};
+      const float4_t B = s_bc[buf][t][0][4 * nt + g];
+      const float de[2] = {d2.x, d2.y}, u[2] = {u2.x, u2.y};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        a[t][i] = exp2_fast(de[i / 4] * A2[i]);
+        a[t][i] = decay(de[i / 4], A2[i]);
         h[t][i] = fmaf(a[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], u[i / 4] * B[i % 4]);
       }
-      if (GATED) {
-        const float4 C4 = s_bc[buf][t][1][4 * nt + g];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          y[t % 2][k] = C4.x * h[t][4 * k] + C4.y * h[t][4 * k + 1] + C4.z * h[t][4 * k + 2] + C4.w * h[t][4 * k + 3];
-        if (t % 2) s_r[w][t / 2][g][dl] = rows(halves(y[0][0], y[0][1]), halves(y[1][0], y[1][1]));
-      }
     }
-    float da[8] = {};
+    float y[2];
 #pragma unroll
     for (int t = T - 1; t >= 0; --t) {
-      const float4 B4 = s_bc[buf][t][0][4 * nt + g], C4 = s_bc[buf][t][1][4 * nt + g];
+      const float4_t B = s_bc[buf][t][0][4 * nt + g], C = s_bc[buf][t][1][4 * nt + g];
       const float2 d2 = s_d[grp][t][dl], u2 = s_u[grp][t][dl], r2 = s_dr[grp][t][dl];
-      const float B[4] = {B4.x, B4.y, B4.z, B4.w}, C[4] = {C4.x, C4.y, C4.z, C4.w};
       const float de[2] = {d2.x, d2.y}, u[2] = {u2.x, u2.y}, r[2] = {r2.x, r2.y};
-      float v[8], s[2] = {}, wa[2] = {};
+      float v[8], s[2], wa[2], yt[2];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = i / 4, n = i % 4;
         const float gi = fmaf(C[n], r[k], ag[i]);
         v[n] = k ? fmaf(gi, u[k], v[n]) : gi * u[k];
         v[4 + n] = k ? fmaf(h[t][i], r[k], v[4 + n]) : h[t][i] * r[k];
-        s[k] = fmaf(gi, B[n], s[k]);
+        s[k] = n ? fmaf(gi, B[n], s[k]) : gi * B[n];
+        if (GATED) yt[k] = n ? fmaf(C[n], h[t][i], yt[k]) : C[n] * h[t][i];
         ag[i] = a[t][i] * gi;
         const float wi = ag[i] * (t ? h[t ? t - 1 : 0][i] : h0[i]);
-        da[i] = fmaf(de[k], wi, da[i]);
-        wa[k] = fmaf(A2[i], wi, wa[k]);
+        dA[i] = fmaf(de[k], wi, dA[i]);
+        wa[k] = n ? fmaf(A2[i], wi, wa[k]) : A2[i] * wi;
       }
       const float v1 = row_sums(v, lane);
       if (lane % 2 == 0) s_part[buf][grp][t][(dl / 8) * N + n0 + dl / 2 % 4] = v1;
       s_red[w][t][g][dl] = rows(halves(s[0], s[1]), halves(wa[0], wa[1]));
+      if (GATED) {
+        y[t % 2] = halves(yt[0], yt[1]);
+        if (t % 2 == 0) s_r[w][t / 2][g][dl] = rows(y[0], y[1]);
+      }
     }
-    // long sums in three steps: eight tokens, 32 blocks, all of them
+    // long sums in two steps: 32 blocks, then those
     const bool flush = blk % 32 == 0 || blk == first;
+    if (flush) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dA2[i] += da[i];
-      if (flush) {
-        dA[i] += dA2[i];
-        dA2[i] = 0.0f;
+      for (int k = 0; k < 2; ++k) {
+        s_dA[k][tid] += (float4_t){dA[4 * k], dA[4 * k + 1], dA[4 * k + 2], dA[4 * k + 3]};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) dA[4 * k + n] = 0.0f;
       }
     }
     group_sync();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int t = blk * T + tok[r], q = tok[r];
-      const bool k = ch[r];
+      const int k = ch(r), o = odd(r), q = 2 * g + o;
       float s = 0.0f, wa = 0.0f, y1 = 0.0f;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         s += s_red[grp * NT + j][q][2 * k][dl];
         wa += s_red[grp * NT + j][q][2 * k + 1][dl];
-        if (GATED) y1 += s_r[grp * NT + j][q / 2][q % 2 + 2 * k][dl];
+        if (GATED) y1 += s_r[grp * NT + j][g][o + 2 * k][dl];
       }
-      const float sk = k ? skip[1] : skip[0];
-      const float dx = fmaf(dlt[r], s, sk * dr[r]), ddt = fmaf(x[r], s, kLn2 * wa) * sg[r], dd = dr[r] * x[r];
-      dskip2[0] += k ? 0.0f : dd;
-      dskip2[1] += k ? dd : 0.0f;
-      dbias2[0] += k ? 0.0f : ddt;
-      dbias2[1] += k ? ddt : 0.0f;
-      if ((k ? in[1] : in[0]) && t < t1) {
-        const size_t o = ((size_t)b * p.S + t) * p.D + (k ? dch[1] : dch[0]);
-        scan_store(static_cast<IO*>(p.dx) + o, dx);
-        scan_store(static_cast<IO*>(p.ddt) + o, ddt);
-        if (GATED) {
-          const float sz = scan_sigmoid(z[r]);
-          scan_store(static_cast<IO*>(p.dz) + o, dy[r] * fmaf(sk, x[r], y1) * sz * (1.0f + z[r] * (1.0f - sz)));
-        }
+      const float4_t item = s_item[r][tid];  // x, sigmoid(dt), dy silu'(z), dr
+      const float sk = k ? skip[1] : skip[0], dlt = reinterpret_cast<const float*>(&s_d[grp][q][dl])[k];
+      const float dx = fmaf(dlt, s, sk * item[3]), ddt = fmaf(item[0], s, kLn2 * wa) * item[1];
+      if constexpr (NT == 4) {  // one channel a wave
+        dskip2[0] = fmaf(item[3], item[0], dskip2[0]);
+        dbias2[0] += ddt;
+      } else {
+        dskip2[r % 2] = fmaf(item[3], item[0], dskip2[r % 2]);
+        dbias2[r % 2] += ddt;
       }
+      const uint32_t off = k ? od[1] : od[0];
+      Raw<IO>::store(rows_at(p.dx, batch, p.D, blk, o), off, dx);
+      Raw<IO>::store(rows_at(p.ddt, batch, p.D, blk, o), off, ddt);
+      if (GATED) Raw<IO>::store(rows_at(p.dz, batch, p.D, blk, o), off, item[2] * fmaf(sk, item[0], y1));
     }
     if (flush) {
 #pragma unroll
@@ -279,17 +306,22 @@ __global__ __launch_bounds__(kThreads) void scan_back_kernel(const ScanParams p)
   __syncthreads();
   if (first < last) add_parts(buf ^ 1, first);
 
-  const size_t part = (size_t)b * p.chunks + c;
+  const size_t part = (size_t)b * p.spans + c;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     if (in[k]) {
-      *reinterpret_cast<float4*>(p.part_a + (part * p.D + dch[k]) * N + n0) =
-          make_float4(dA[4 * k], dA[4 * k + 1], dA[4 * k + 2], dA[4 * k + 3]);
+      *reinterpret_cast<float4_t*>(p.part_a + (part * p.D + dch[k]) * N + n0) = s_dA[k][tid];
       if (c == 0 && p.dh0)
         *reinterpret_cast<float4*>(p.dh0 + ((size_t)b * p.D + dch[k]) * N + n0) =
             make_float4(ag[4 * k], ag[4 * k + 1], ag[4 * k + 2], ag[4 * k + 3]);
     }
   // dD and dbias of a channel: over the lanes that have it, then over the waves of the group
+  if constexpr (NT == 4) {
+    dskip[1] = nt % 2 ? dskip[0] : 0.0f;
+    dbias[1] = nt % 2 ? dbias[0] : 0.0f;
+    dskip[0] = nt % 2 ? 0.0f : dskip[0];
+    dbias[0] = nt % 2 ? 0.0f : dbias[0];
+  }
   s_red[w][0][g][dl] = rows(halves(dskip[0], dskip[1]), halves(dbias[0], dbias[1]));
   group_sync();
   if (nt == 0) {
@@ -319,7 +351,7 @@ __global__ __launch_bounds__(kThreads) void scan_back_columns_kernel(const ScanP
 // dA, dD and dbias: the parts of the chunks, in order.
 __global__ __launch_bounds__(kThreads) void scan_back_sums_kernel(const ScanParams p) {
   const int64_t na = (int64_t)p.D * p.N, n = na + 2 * p.D;
-  const int parts = p.S > 0 ? p.B * p.chunks : 0;
+  const int parts = p.S > 0 ? p.B * p.spans : 0;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
     float s = 0.0f;
     const float* from = i < na ? p.part_a + i : p.part_d + (i - na);
@@ -350,7 +382,7 @@ unsigned groups_for(int64_t threads) {
 template <typename IO, int N>
 hipError_t launch_gated(const ScanParams& p, hipStream_t stream) {
   const unsigned nd = (unsigned)((p.D + scan_back_channels(N) - 1) / scan_back_channels(N));
-  const dim3 grid(nd * (unsigned)p.chunks * (unsigned)p.B);
+  const dim3 grid(nd * (unsigned)p.spans * (unsigned)p.B);
   if (p.z.p)
     hipLaunchKernelGGL((scan_back_kernel<IO, N, true>), grid, dim3(kThreads), 0, stream, p);
   else

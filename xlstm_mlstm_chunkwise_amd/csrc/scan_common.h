@@ -14,27 +14,30 @@ __device__ __forceinline__ void scan_store(float* p, float x) { *p = x; }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// exp(d A) with A2 = A log2(e).  The instruction is low by 1e-9 to 6e-9 of the
+// value on average near exponents of zero (rounding apart, over 2^20 values), and
+// a slow state multiplies thousands of these; the addend, for free in the fused
+// product, takes that out.  d = 0 gives 1.
+__device__ __forceinline__ float decay(float d, float A2) { return exp2_fast(fmaf(d, A2, 4e-9f)); }
+
 // 1 / (1 + e^-x)
 __device__ __forceinline__ float scan_sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + exp2_fast(-kLog2e * x));
 }
 
 // log(1 + e^x) = max(x, 0) + log(1 + e),  e = e^-|x| in (0, 1].  With s = e /
-// (2 + e) <= 1/3, log(1 + e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...): the
-// terms from s^16 on are below 1.4e-9 of the sum, and a small e keeps its
-// digits (log(1 + e) of a rounded 1 + e does not).
+// (2 + e) <= 1/3, log(1 + e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...); the
+// bracket is a polynomial in s^2 fitted at Chebyshev points of [0, 1/9], off by
+// 4e-9.  A small e keeps its digits (log(1 + e) of a rounded 1 + e does not).
 __device__ __forceinline__ float softplus(float x) {
   const float e = exp2_fast(-kLog2e * fabsf(x));
   const float s = e * __builtin_amdgcn_rcpf(2.0f + e), q = s * s;
-  float p = 1.0f / 15.0f;
-  p = fmaf(p, q, 1.0f / 13.0f);
-  p = fmaf(p, q, 1.0f / 11.0f);
-  p = fmaf(p, q, 1.0f / 9.0f);
-  p = fmaf(p, q, 1.0f / 7.0f);
-  p = fmaf(p, q, 1.0f / 5.0f);
-  p = fmaf(p, q, 1.0f / 3.0f);
-  p = fmaf(p, q, 1.0f);
-  return fmaxf(x, 0.0f) + 2.0f * s * p;
+  float p = 0.28174657f;
+  p = fmaf(p, q, 0.27961419f);
+  p = fmaf(p, q, 0.40024854f);
+  p = fmaf(p, q, 0.66666316f);
+  p = fmaf(p, q, 2.0f);
+  return fmaf(s, p, fmaxf(x, 0.0f));
 }
 
 // Values as they are in memory, and how a float becomes one.
@@ -70,7 +73,7 @@ constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // outside of every resource
 template <typename T, int ROWS>
 struct RowWindow {
   const T* base;
-  uint32_t stride;  // bytes; below 2^28
+  uint32_t stride;  // bytes; below 2^27
   uint32_t off[ROWS];
   __device__ __forceinline__ void init(const void* p, int64_t batch, int64_t token, uint32_t column, bool in) {
     base = static_cast<const T*>(p) + batch;

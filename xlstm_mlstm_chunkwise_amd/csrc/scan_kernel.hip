@@ -2,28 +2,33 @@
 //   d = softplus(dt + bias),  u = d x
 //   h = exp(d A) h + u B,  y = (C . h + D x) z sigmoid(z)
 //
-// A workgroup has 64 channels, one a lane, and four waves, which have a quarter
+// A workgroup has 64 channels, one a lane, and eight waves, which have an eighth
 // of the N states each: h stays in registers.  B and C are the same for a whole
 // wave; they are taken from a float32 copy by scalar loads and are scalar
-// operands.  Tiles of sixteen tokens: a wave turns x and dt of four of them into
-// d and u for all waves through LDS, walks the sixteen tokens with its states,
-// and leaves its part of C . h in LDS, where the waves add four tokens each.
+// operands.  Tiles of sixteen tokens: a wave turns x and dt of two of them into d
+// and u for all waves through LDS, walks the sixteen tokens with its states, and
+// leaves its part of C . h in LDS, where the waves add two tokens each.
 //
 // Few channels leave compute units idle: the sequence is then cut into chunks
 // that are walked side by side, first each from a zero state (what it leaves,
 // and the sum of d, whose product with A is the log of the chunk's decay), then
 // from the state that the chunks before it leave.
+#include <type_traits>
+
 #include "scan_common.h"
 
 namespace mlstm {
 namespace {
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves, kQuad = 4;
-static_assert(kScanTile == kWaves * kQuad, "a wave prepares four tokens of a tile");
+constexpr int kWaves = kScanWaves, kThreads = 64 * kWaves;
+constexpr int kQuads = kScanTile / 4;           // LDS holds four tokens of a channel together
+constexpr int kOwn = kScanTile / kWaves;        // tokens of a tile that a wave prepares and finishes
+typedef float own_t __attribute__((ext_vector_type(kOwn)));
 
 // Read-only memory at an address that a whole wave shares.
 typedef const float __attribute__((address_space(4)))* uniform_t;
-typedef const float4_t __attribute__((address_space(4)))* uniform4_t;
+typedef float float16_t __attribute__((ext_vector_type(16)));
+typedef const float16_t __attribute__((address_space(4)))* uniform16_t;
 
 // The value is waited for here.
 __device__ __forceinline__ void arrived(float x) { asm volatile("" ::"s"(x)); }
@@ -35,7 +40,7 @@ enum class Mode {
   kOutput,  // y and the final state
   kEnds,    // what a chunk leaves of a zero state, and its sum of d
   kKept,    // the state in front of every eight tokens
-  kBoth     // kEnds, and the state gradient that a chunk hands on by itself
+  kSpans    // kKept, and for every span its sum of d and the state gradient that it hands on by itself
 };
 
 template <typename T>
@@ -54,21 +59,21 @@ __device__ __forceinline__ void enter(const ScanParams& p, int b, int c, int d, 
     const size_t i = ((size_t)b * p.chunks + k) * p.D + d;
     const float s = p.sums[i];
 #pragma unroll
-    for (int r = 0; r < NPW; ++r) h[r] = fmaf(exp2_fast(s * A2[r]), h[r], p.ends[i * p.N + n0 + r]);
+    for (int r = 0; r < NPW; ++r) h[r] = fmaf(decay(s, A2[r]), h[r], p.ends[i * p.N + n0 + r]);
   }
 }
 
 template <typename T, int N, Mode MODE, bool GATED>
 __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
-  constexpr int NPW = N / kWaves;
-  constexpr bool OUT = MODE == Mode::kOutput, BACK = MODE == Mode::kBoth, ENTER = OUT || MODE == Mode::kKept;
+  constexpr int NPW = N / kWaves;          // states of a wave
+  constexpr bool OUT = MODE == Mode::kOutput, BACK = MODE == Mode::kSpans, KEEP = MODE == Mode::kKept || BACK;
+  constexpr bool ENTER = MODE != Mode::kEnds;
   constexpr bool COLS = OUT || BACK;      // C is read
-  // tokens whose B and C are held at a time: sixteen scalar registers, and sixteen on their way
-  constexpr int GROUP = (COLS ? 8 : 16) > NPW ? (COLS ? 8 : 16) / NPW : 1;
-  constexpr int GROUPS = kScanTile / GROUP, PER_QUAD = kQuad / GROUP;
-  __shared__ float4_t s_d[2][kWaves][64], s_u[2][kWaves][64];
-  __shared__ float4_t s_g[BACK ? 2 : 1][kWaves][64];
-  __shared__ float4_t s_y[OUT ? 2 : 1][kWaves][kWaves][64];
+  constexpr int GROUP = 16 / NPW;         // tokens whose B, or C, one scalar load of 64 bytes brings
+  constexpr int GROUPS = kScanTile / GROUP;
+  __shared__ float4_t s_d[2][kQuads][64], s_u[2][kQuads][64];
+  __shared__ float4_t s_g[BACK ? 2 : 1][kQuads][64];
+  __shared__ float4_t s_y[OUT ? 2 : 1][kWaves][kQuads][64];
 
   const int nd = (p.D + kScanChannels - 1) / kScanChannels;
   const int db = blockIdx.x % nd, bc = blockIdx.x / nd, c = bc % p.chunks, b = bc / p.chunks;
@@ -83,51 +88,52 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
   float A2[NPW], h[NPW], W[NPW], G[NPW];
 #pragma unroll
   for (int r = 0; r < NPW; ++r) A2[r] = kLog2e * p.A[(size_t)d * N + n0 + r];
-  if (ENTER) {
-    enter<NPW>(p, b, c, d, n0, A2, h);
-  } else {
 #pragma unroll
-    for (int r = 0; r < NPW; ++r) {
-      h[r] = G[r] = 0.0f;
-      W[r] = 1.0f;
-    }
+  for (int r = 0; r < NPW; ++r) {
+    h[r] = G[r] = 0.0f;
+    W[r] = 1.0f;
   }
+  if (ENTER) enter<NPW>(p, b, c, d, n0, A2, h);
 
   typedef typename Raw<T>::type raw_t;
-  RowWindow<T, kQuad> vx, vdt, vz, vdy, vy;
+  RowWindow<T, kOwn> vx, vdt, vz, vdy, vy;
   vx.init(p.x.p, b * p.x.batch, p.x.token, d, true);
   vdt.init(p.dt.p, b * p.dt.batch, p.dt.token, d, true);
   if (GATED) vz.init(p.z.p, b * p.z.batch, p.z.token, d, true);
   if (BACK) vdy.init(p.dy, (int64_t)b * p.S * p.D, p.D, d, true);
   if (OUT) vy.init(p.y, (int64_t)b * p.S * p.D, p.D, d, in);
 
-  raw_t rx[kQuad], rdt[kQuad], rz[kQuad], rdy[kQuad];
-  float x[kQuad], sum = 0.0f;
+  raw_t rx[kOwn], rdt[kOwn], rz[kOwn], rdy[kOwn];
+  float sum = 0.0f;
+  // this wave's tokens among a tile's, four of a channel together
+  auto own = [&](float4_t* tile) -> own_t& {
+    return *reinterpret_cast<own_t*>(reinterpret_cast<float*>(&tile[kOwn * w / 4 * 64 + lane]) + kOwn * w % 4);
+  };
   auto fetch = [&](int t) {
-    const int tq = t + kQuad * w;
+    const int tq = t + kOwn * w;
     const auto ax = vx.at(tq, t1), adt = vdt.at(tq, t1);
 #pragma unroll
-    for (int j = 0; j < kQuad; ++j) rx[j] = Raw<T>::load(ax, vx.off[j]);
+    for (int j = 0; j < kOwn; ++j) rx[j] = Raw<T>::load(ax, vx.off[j]);
 #pragma unroll
-    for (int j = 0; j < kQuad; ++j) rdt[j] = Raw<T>::load(adt, vdt.off[j]);
+    for (int j = 0; j < kOwn; ++j) rdt[j] = Raw<T>::load(adt, vdt.off[j]);
     if (BACK) {
       const auto ady = vdy.at(tq, t1);
 #pragma unroll
-      for (int j = 0; j < kQuad; ++j) rdy[j] = Raw<T>::load(ady, vdy.off[j]);
+      for (int j = 0; j < kOwn; ++j) rdy[j] = Raw<T>::load(ady, vdy.off[j]);
       if (GATED) {
         const auto az = vz.at(tq, t1);
 #pragma unroll
-        for (int j = 0; j < kQuad; ++j) rz[j] = Raw<T>::load(az, vz.off[j]);
+        for (int j = 0; j < kOwn; ++j) rz[j] = Raw<T>::load(az, vz.off[j]);
       }
     }
   };
   // Tokens behind the chunk's end have d = u = 0 and leave the state.
-  auto prepare = [&](int buf, int t) {
-    float4_t dl, u, g;
+  auto prepare = [&](int buf, int t, own_t& x) {
+    own_t dl, u, g;
 #pragma unroll
-    for (int j = 0; j < kQuad; ++j) {
+    for (int j = 0; j < kOwn; ++j) {
       const float step = softplus(Raw<T>::value(rdt[j]) + bias);
-      dl[j] = t + kQuad * w + j < t1 ? step : 0.0f;
+      dl[j] = t + kOwn * w + j < t1 ? step : 0.0f;
       x[j] = Raw<T>::value(rx[j]);
       u[j] = dl[j] * x[j];
       if (BACK) {
@@ -136,123 +142,147 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
         if (GATED) g[j] *= z * scan_sigmoid(z);
       }
     }
-    s_d[buf][w][lane] = dl;
-    s_u[buf][w][lane] = u;
-    if (BACK) s_g[buf][w][lane] = g;
+    own(s_d[buf][0]) = dl;
+    own(s_u[buf][0]) = u;
+    if (BACK) own(s_g[buf][0]) = g;
   };
 
-  // B and C of a group of tokens, and d, u (and dr) of four, are asked for while
-  // the group before is worked on.  Scalar loads come back in any order, so the
-  // one wait for them is for all: it stands before the next are asked for.
-  const uniform_t cols = (uniform_t)(uintptr_t)(p.bc + (size_t)b * p.rows * 2 * N + n0);
-  float4_t nB[GROUP][NPW / 4], nC[GROUP][NPW / 4], B[GROUP][NPW / 4], C[GROUP][NPW / 4];
-  float4_t nd4, nu4, ng4, d4, u4, g4;
-  auto ask = [&](int t) {
-#pragma unroll
-    for (int j = 0; j < GROUP; ++j)
-#pragma unroll
-      for (int r = 0; r < NPW / 4; ++r) {
-        const uniform_t at = cols + (size_t)t * 2 * N + j * 2 * N + 4 * r;
-        nB[j][r] = *(uniform4_t)at;
-        if (COLS) nC[j][r] = *(uniform4_t)(at + N);
-      }
+  // B and C of a group of tokens, and d, u (and dr) of the next four or eight, are
+  // asked for while the group before is worked on.  Scalar loads come back in any
+  // order, so the one wait for them is for all: it stands before the next are
+  // asked for.
+  const uniform_t cols = (uniform_t)(uintptr_t)(p.bc + (size_t)b * p.rows * 2 * N + w * 32);
+  constexpr int QG = GROUP > 4 ? GROUP / 4 : 1;  // quads a group has
+  float16_t nB, nC;
+  float4_t d4[2][QG], u4[2][QG], g4[2][QG];  // two sets in turn
+  auto ask = [&](int t, int i) {  // group i of the tile from t on
+    const uniform_t at = cols + (size_t)t * 2 * N + i * (32 * kWaves);
+    nB = *(uniform16_t)at;
+    if (COLS) nC = *(uniform16_t)(at + 16);
   };
-  auto ask_quad = [&](int buf, int q) {
-    nd4 = s_d[buf][q][lane];
-    nu4 = s_u[buf][q][lane];
-    if (BACK) ng4 = s_g[buf][q][lane];
-  };
-
-  if (t0 < t1) {
-    fetch(t0);
-    ask(t0);
-    prepare(0, t0);
-    fetch(t0 + kScanTile);
-  }
-  __syncthreads();
-  if (t0 < t1) ask_quad(0, 0);
-  int buf = 0;
-  for (int t = t0; t < t1; t += kScanTile, buf ^= 1) {
-    float xk[kQuad];
-    float4_t y;
+  auto ask_quads = [&](int buf, int q, int set) {
 #pragma unroll
-    for (int j = 0; j < kQuad; ++j) xk[j] = x[j];
-    if (OUT && GATED) {
-      const auto az = vz.at(t + kQuad * w, t1);
-#pragma unroll
-      for (int j = 0; j < kQuad; ++j) rz[j] = Raw<T>::load(az, vz.off[j]);
+    for (int k = 0; k < QG; ++k) {
+      d4[set][k] = s_d[buf][q + k][lane];
+      u4[set][k] = s_u[buf][q + k][lane];
+      if (BACK) g4[set][k] = s_g[buf][q + k][lane];
     }
+  };
+
+  // y of a tile whose parts of C . h are in LDS
+  auto finish = [&](int buf, int t, const own_t& x) {
+    own_t s = own(s_y[buf][0][0]);
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) s += own(s_y[buf][k][0]);
+    const auto ay = vy.at(t + kOwn * w, t1);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      float v = fmaf(skip, x[j], s[j]);
+      const float z = GATED ? Raw<T>::value(rz[j]) : 0.0f;
+      if (GATED) v *= z * scan_sigmoid(z);
+      Raw<T>::store(ay, vy.off[j], v);
+    }
+  };
+
+  own_t x[2];  // of the tiles in the two buffers
+  // A tile: its d and u are in buffer BUF, B and C of its first group on their way.
+  auto tile = [&](auto which, int t) {
+    constexpr int BUF = decltype(which)::value;
+    const bool more = t + kScanTile < t1;
+    float4_t y;
+    ask_quads(BUF, 0, 0);
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i) {
-      const int q = i / PER_QUAD, j0 = i % PER_QUAD * GROUP;
-#pragma unroll
-      for (int j = 0; j < GROUP; ++j)
-#pragma unroll
-        for (int r = 0; r < NPW / 4; ++r) {
-          B[j][r] = nB[j][r];
-          if (COLS) C[j][r] = nC[j][r];
-          arrived(B[j][r][0]);
-        }
+      const int q = i * GROUP / 4, j0 = i * GROUP % 4, set = q / QG % 2;
+      const float16_t B = nB, C = nC;
+      arrived(B[0]);
+      if (COLS) arrived(C[0]);
       if (j0 == 0) {
-        d4 = nd4;
-        u4 = nu4;
-        if (BACK) g4 = ng4;
-        arrived_lane(d4[0]);
-        arrived_lane(u4[0]);
-        if (BACK) arrived_lane(g4[0]);
-        if (q + 1 < kWaves) ask_quad(buf, q + 1);
+#pragma unroll
+        for (int k = 0; k < QG; ++k) {
+          arrived_lane(d4[set][k][0]);
+          arrived_lane(u4[set][k][0]);
+          if (BACK) arrived_lane(g4[set][k][0]);
+        }
+        if (q + QG < kQuads) ask_quads(BUF, q + QG, set ^ 1);
       }
       // behind the last tile, the same tile again
-      ask(i + 1 < GROUPS ? t + (i + 1) * GROUP : t + kScanTile < t1 ? t + kScanTile : t);
+      ask(i + 1 < GROUPS || !more ? t : t + kScanTile, (i + 1) % GROUPS);
       __builtin_amdgcn_sched_barrier(0);
-      if (MODE == Mode::kKept && i % (GROUPS / 2) == 0 && in) {
-        float* to = p.kept + (((size_t)b * (p.rows / kScanBlock) + t / kScanBlock + q / 2) * p.D + d) * N + n0;
+      if (KEEP && i * GROUP % kScanBlock == 0 && in) {
+        const size_t block = (size_t)b * (p.rows / kScanBlock) + (t + i * GROUP) / kScanBlock;
+        float2* to = reinterpret_cast<float2*>(p.kept) + (block * (N / 2) + n0 / 2) * p.D + d;
 #pragma unroll
-        for (int r = 0; r < NPW; r += 4) *reinterpret_cast<float4*>(to + r) = make_float4(h[r], h[r + 1], h[r + 2], h[r + 3]);
+        for (int r = 0; r < NPW / 2; ++r) to[(size_t)r * p.D] = make_float2(h[2 * r], h[2 * r + 1]);
       }
 #pragma unroll
       for (int j = 0; j < GROUP; ++j) {
         const int k = j0 + j;
+        const float dk = d4[set][k / 4][k % 4], uk = u4[set][k / 4][k % 4];
         float yk = 0.0f;
-        if (!ENTER) sum += d4[k];
+        if (!ENTER || BACK) sum += dk;
 #pragma unroll
         for (int r = 0; r < NPW; ++r) {
-          const float a = exp2_fast(d4[k] * A2[r]);
-          h[r] = fmaf(a, h[r], u4[k] * B[j][r / 4][r % 4]);
-          if (OUT) yk = fmaf(C[j][r / 4][r % 4], h[r], yk);
+          const float a = decay(dk, A2[r]);
+          h[r] = fmaf(a, h[r], uk * B[j * NPW + r]);
+          if (OUT) yk = r ? fmaf(C[j * NPW + r], h[r], yk) : C[j * NPW + r] * h[r];
           if (BACK) {
             W[r] *= a;
-            G[r] = fmaf(C[j][r / 4][r % 4], W[r] * g4[k], G[r]);
+            G[r] = fmaf(C[j * NPW + r], W[r] * g4[set][k / 4][k % 4], G[r]);
           }
         }
-        y[k] = yk;
+        y[k % 4] = yk;
+        if (OUT && k % 4 == 3) s_y[BUF][w][q + k / 4][lane] = y;
       }
 #pragma unroll
       for (int r = 0; r < NPW; ++r) {
         formed(h[r]);
         if (BACK) formed(G[r]);
       }
-      if (OUT && j0 + GROUP == kQuad) s_y[buf][w][q][lane] = y;
+      // the tile before, while the next group's operands come
+      if (OUT && i == 0) {
+        if (t > t0) finish(BUF ^ 1, t - kScanTile, x[BUF ^ 1]);
+        if (GATED) {
+          const auto az = vz.at(t + kOwn * w, t1);
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) rz[j] = Raw<T>::load(az, vz.off[j]);
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
-    const bool more = t + kScanTile < t1;
+    if (BACK && (!more || (t + kScanTile) % p.span == 0)) {
+      const size_t i = ((size_t)b * p.spans + t / p.span) * p.D + d;
+#pragma unroll
+      for (int r = 0; r < NPW; ++r) {
+        if (in) p.grads[i * N + n0 + r] = G[r];
+        G[r] = 0.0f;
+        W[r] = 1.0f;
+      }
+      if (in && w == 0) p.span_sums[i] = sum;
+      sum = 0.0f;
+    }
     if (more) {
-      prepare(buf ^ 1, t + kScanTile);
+      prepare(BUF ^ 1, t + kScanTile, x[BUF ^ 1]);
       fetch(t + 2 * kScanTile);
     }
     __syncthreads();
-    if (more) ask_quad(buf ^ 1, 0);
-    if (OUT) {
-      float4_t s = s_y[buf][0][w][lane];
-#pragma unroll
-      for (int k = 1; k < kWaves; ++k) s += s_y[buf][k][w][lane];
-      const auto ay = vy.at(t + kQuad * w, t1);
-#pragma unroll
-      for (int j = 0; j < kQuad; ++j) {
-        float v = fmaf(skip, xk[j], s[j]);
-        const float z = GATED ? Raw<T>::value(rz[j]) : 0.0f;
-        if (GATED) v *= z * scan_sigmoid(z);
-        Raw<T>::store(ay, vy.off[j], v);
+  };
+  if (t0 < t1) {
+    fetch(t0);
+    ask(t0, 0);
+    prepare(0, t0, x[0]);
+    fetch(t0 + kScanTile);
+    __syncthreads();
+    for (int t = t0;; t += 2 * kScanTile) {
+      tile(std::integral_constant<int, 0>{}, t);
+      if (t + kScanTile >= t1) {
+        if (OUT) finish(0, t, x[0]);
+        break;
+      }
+      tile(std::integral_constant<int, 1>{}, t + kScanTile);
+      if (t + 2 * kScanTile >= t1) {
+        if (OUT) finish(1, t + kScanTile, x[1]);
+        break;
       }
     }
   }
@@ -264,25 +294,22 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
   } else if (!ENTER) {
     const size_t i = ((size_t)b * p.chunks + c) * p.D + d;
 #pragma unroll
-    for (int r = 0; r < NPW; ++r) {
-      p.ends[i * N + n0 + r] = h[r];
-      if (BACK) p.grads[i * N + n0 + r] = G[r];
-    }
+    for (int r = 0; r < NPW; ++r) p.ends[i * N + n0 + r] = h[r];
     if (w == 0) p.sums[i] = sum;
   }
 }
 
-// Bm and Cm in float32, token after token, zeros behind the sequence.
+// Bm and Cm in float32 as the waves read them, zeros behind the sequence.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void scan_columns_kernel(const ScanParams p) {
+__global__ __launch_bounds__(256) void scan_columns_kernel(const ScanParams p) {
+  const int tile = kScanTile * 2 * p.N;
   const int64_t n = (int64_t)p.B * p.rows * 2 * p.N;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-    const int col = (int)(i % (2 * p.N));
-    const int64_t row = i / (2 * p.N);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t q = i / tile;
+    const ScanColumn c = scan_column((int)(i - q * tile), p.N);
+    const int64_t row = q * kScanTile + c.token;
     const int b = (int)(row / p.rows), t = (int)(row - (int64_t)b * p.rows);
-    float v = 0.0f;
-    if (t < p.S) v = col < p.N ? at<T>(p.Bm, b, t, col) : at<T>(p.Cm, b, t, col - p.N);
-    p.bc[i] = v;
+    p.bc[i] = t < p.S ? at<T>(c.which ? p.Cm : p.Bm, b, t, c.state) : 0.0f;
   }
 }
 
@@ -313,25 +340,41 @@ hipError_t launch(const ScanParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_columns(const ScanParams& p, hipStream_t stream) {
-  const int64_t n = ((int64_t)p.B * p.rows * 2 * p.N + kThreads - 1) / kThreads;
+  const int64_t n = ((int64_t)p.B * p.rows * 2 * p.N + 255) / 256;
   const dim3 grid((unsigned)(n < (1 << 16) ? n : 1 << 16));
   if (p.bf16)
-    hipLaunchKernelGGL(scan_columns_kernel<bf16_t>, grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL(scan_columns_kernel<bf16_t>, grid, dim3(256), 0, stream, p);
   else
-    hipLaunchKernelGGL(scan_columns_kernel<float>, grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL(scan_columns_kernel<float>, grid, dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int scan_chunks(int B, int S, int D, int N, bool back) {
-  const int width = back ? scan_back_channels(N) : kScanChannels;
-  const int64_t groups = (int64_t)B * ((D + width - 1) / width), tiles = ((int64_t)S + kScanTile - 1) / kScanTile;
-  const int64_t most = back ? 256 : 768;
-  int64_t n = groups > most / 3 ? 1 : most / groups;
-  if (n > tiles / 4) n = tiles / 4;
-  if (n > 64) n = 64;
-  return (int)(n < 1 ? 1 : n);
+void scan_cut(ScanParams& p, bool back) {
+  const int tiles = p.rows / kScanTile;
+  // n pieces of whole tiles, four at least; every one has tokens
+  auto cut = [&](int64_t n, int* pieces, int* length) {
+    if (n > tiles / 4) n = tiles / 4;
+    if (n > 64) n = 64;
+    if (n < 1) n = 1;
+    *length = (int)((tiles + n - 1) / n) * kScanTile;
+    *pieces = *length ? (p.S + *length - 1) / *length : 1;
+  };
+  // 512 workgroups are there at a time, two a compute unit
+  const int64_t groups = (int64_t)p.B * ((p.D + kScanChannels - 1) / kScanChannels);
+  cut(groups <= 256 ? 512 / groups : 1, &p.chunks, &p.chunk);
+  p.spans = p.chunks;
+  p.span = p.chunk;
+  if (back) {
+    const int ch = scan_back_channels(p.N);
+    cut(512 / ((int64_t)p.B * ((p.D + ch - 1) / ch)), &p.spans, &p.span);
+    // whole spans in a chunk
+    if (p.chunks > 1) {
+      p.chunk = (p.chunk + p.span - 1) / p.span * p.span;
+      p.chunks = (p.S + p.chunk - 1) / p.chunk;
+    }
+  }
 }
 
 hipError_t launch_scan(const ScanParams& p, hipStream_t stream) {
@@ -343,8 +386,8 @@ hipError_t launch_scan(const ScanParams& p, hipStream_t stream) {
 
 hipError_t launch_scan_states(const ScanParams& p, hipStream_t stream) {
   hipError_t e = launch_columns(p, stream);
-  if (e == hipSuccess && p.chunks > 1) e = launch<Mode::kBoth>(p, stream);
-  if (e == hipSuccess) e = launch<Mode::kKept>(p, stream);
+  if (e == hipSuccess && p.chunks > 1) e = launch<Mode::kEnds>(p, stream);
+  if (e == hipSuccess) e = p.spans > 1 ? launch<Mode::kSpans>(p, stream) : launch<Mode::kKept>(p, stream);
   return e;
 }
 
