@@ -88,7 +88,11 @@ __global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams
   __shared__ float s_red[kWaves][T][4][16];
   __shared__ float s_r[GATED ? kWaves : 1][T / 2][4][16];
   __shared__ float4_t s_item[R][kThreads];          // x, sigmoid(dt), dy silu'(z), dy silu(z)
-  __shared__ float4_t s_dA[2][kThreads];
+  // What a lane needs once a block stays in LDS: a register more would spill, and
+  // a spilled one comes back behind the loads of the next block.
+  __shared__ float4_t s_dA[2][kThreads], s_dD[2][kThreads];  // dD and dbias of both channels, in two steps
+  __shared__ float4_t s_scalar[kThreads];                    // dt_bias and D of both channels
+  __shared__ uint4 s_off[2][kThreads];                       // offsets of x, dt; z, dy of both channels
 
   const int nd = (p.D + CH - 1) / CH;
   const int db = blockIdx.x % nd, bc = blockIdx.x / nd, c = bc % p.spans, b = bc / p.spans;
@@ -125,25 +129,23 @@ __global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams
         const_cast<char*>(static_cast<const char*>(base)) + (b * batch + t * stride) * (int64_t)sizeof(IO), 0,
         n * (int)stride * (int)sizeof(IO), 0x00020000);
   };
-  uint32_t ox[2], odt[2], oz[2], od[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    ox[k] = offset(p.x.token, k);
-    odt[k] = offset(p.dt.token, k);
-    if (GATED) oz[k] = offset(p.z.token, k);
-    od[k] = offset(p.D, k);
-  }
+  s_off[0][tid] = make_uint4(offset(p.x.token, 0), offset(p.x.token, 1), offset(p.dt.token, 0), offset(p.dt.token, 1));
+  s_off[1][tid] = make_uint4(GATED ? offset(p.z.token, 0) : 0, GATED ? offset(p.z.token, 1) : 0, offset(p.D, 0), offset(p.D, 1));
+  s_scalar[tid] = (float4_t){p.bias ? p.bias[dch[0]] : 0.0f, p.bias ? p.bias[dch[1]] : 0.0f,
+                             p.Dskip ? p.Dskip[dch[0]] : 0.0f, p.Dskip ? p.Dskip[dch[1]] : 0.0f};
+  s_dD[0][tid] = s_dD[1][tid] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
   const int64_t batch = (int64_t)p.S * p.D;
   raw_t rx[R], rdt[R], rdy[R], rz[R];
   float rbc[PER];
   auto fetch = [&](int blk) {
+    const uint4 oa = s_off[0][tid], ob = s_off[1][tid];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int o = odd(r), k = ch(r);
-      rx[r] = Raw<IO>::load(rows_at(p.x.p, p.x.batch, p.x.token, blk, o), k ? ox[1] : ox[0]);
-      rdt[r] = Raw<IO>::load(rows_at(p.dt.p, p.dt.batch, p.dt.token, blk, o), k ? odt[1] : odt[0]);
-      rdy[r] = Raw<IO>::load(rows_at(p.dy, batch, p.D, blk, o), k ? od[1] : od[0]);
-      if (GATED) rz[r] = Raw<IO>::load(rows_at(p.z.p, p.z.batch, p.z.token, blk, o), k ? oz[1] : oz[0]);
+      rx[r] = Raw<IO>::load(rows_at(p.x.p, p.x.batch, p.x.token, blk, o), k ? oa.y : oa.x);
+      rdt[r] = Raw<IO>::load(rows_at(p.dt.p, p.dt.batch, p.dt.token, blk, o), k ? oa.w : oa.z);
+      rdy[r] = Raw<IO>::load(rows_at(p.dy, batch, p.D, blk, o), k ? ob.w : ob.z);
+      if (GATED) rz[r] = Raw<IO>::load(rows_at(p.z.p, p.z.batch, p.z.token, blk, o), k ? ob.y : ob.x);
     }
     const float* from = p.bc + ((size_t)b * p.rows + blk * T) * 2 * N;
 #pragma unroll
@@ -175,16 +177,13 @@ __global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams
     else
       wave_sync();
   };
-  const float bias[2] = {p.bias ? p.bias[dch[0]] : 0.0f, p.bias ? p.bias[dch[1]] : 0.0f};
-  const float skip[2] = {p.Dskip ? p.Dskip[dch[0]] : 0.0f, p.Dskip ? p.Dskip[dch[1]] : 0.0f};
-
-  float dskip[2] = {}, dbias[2] = {}, dskip2[2] = {}, dbias2[2] = {};
   if (first < last) {
     fetch(last - 1);
     fetch_state(last - 1);
   }
   int buf = 0;
   for (int blk = last - 1; blk >= first; --blk, buf ^= 1) {
+    const float4_t bias = s_scalar[tid];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int k = ch(r), q = 2 * g + odd(r);
@@ -209,15 +208,18 @@ __global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams
     }
     __syncthreads();
     if (blk < last - 1) add_parts(buf ^ 1, blk + 1);
-    if (blk > first) fetch(blk - 1);
-
     float h0[8], a[T][8], h[T][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       h0[2 * i] = in[i / 2] ? rh[i].x : 0.0f;
       h0[2 * i + 1] = in[i / 2] ? rh[i].y : 0.0f;
     }
-    if (blk > first) fetch_state(blk - 1);
+    // h0 is there before the next loads go out: a wait for it behind them would be for them too.  In front of the
+    // first block, the first again: a branch would make the waits behind it the longer ones of both ways.
+#pragma unroll
+    for (int i = 0; i < 8; ++i) formed(h0[i]);
+    fetch(max(blk - 1, first));
+    fetch_state(max(blk - 1, first));
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const float2 d2 = s_d[grp][t][dl], u2 = s_u[grp][t][dl];
@@ -268,6 +270,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams
       }
     }
     group_sync();
+    const float4_t scalar = s_scalar[tid];
+    float4_t sums = s_dD[0][tid];
+    const uint4 ob = s_off[1][tid];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int k = ch(r), o = odd(r), q = 2 * g + o;
@@ -279,28 +284,21 @@ __global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams
         if (GATED) y1 += s_r[grp * NT + j][g][o + 2 * k][dl];
       }
       const float4_t item = s_item[r][tid];  // x, sigmoid(dt), dy silu'(z), dr
-      const float sk = k ? skip[1] : skip[0], dlt = reinterpret_cast<const float*>(&s_d[grp][q][dl])[k];
+      const float sk = k ? scalar[3] : scalar[2], dlt = reinterpret_cast<const float*>(&s_d[grp][q][dl])[k];
       const float dx = fmaf(dlt, s, sk * item[3]), ddt = fmaf(item[0], s, kLn2 * wa) * item[1];
-      if constexpr (NT == 4) {  // one channel a wave
-        dskip2[0] = fmaf(item[3], item[0], dskip2[0]);
-        dbias2[0] += ddt;
-      } else {
-        dskip2[r % 2] = fmaf(item[3], item[0], dskip2[r % 2]);
-        dbias2[r % 2] += ddt;
-      }
-      const uint32_t off = k ? od[1] : od[0];
+      const int sum = NT == 4 ? 0 : r % 2;  // one channel a wave, or both
+      sums[sum] = fmaf(item[3], item[0], sums[sum]);
+      sums[2 + sum] += ddt;
+      const uint32_t off = k ? ob.w : ob.z;
       Raw<IO>::store(rows_at(p.dx, batch, p.D, blk, o), off, dx);
       Raw<IO>::store(rows_at(p.ddt, batch, p.D, blk, o), off, ddt);
       if (GATED) Raw<IO>::store(rows_at(p.dz, batch, p.D, blk, o), off, item[2] * fmaf(sk, item[0], y1));
     }
     if (flush) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        dskip[k] += dskip2[k];
-        dbias[k] += dbias2[k];
-        dskip2[k] = dbias2[k] = 0.0f;
-      }
+      s_dD[1][tid] += sums;
+      sums = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
     }
+    s_dD[0][tid] = sums;
     group_sync();
   }
   __syncthreads();
@@ -316,13 +314,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams
             make_float4(ag[4 * k], ag[4 * k + 1], ag[4 * k + 2], ag[4 * k + 3]);
     }
   // dD and dbias of a channel: over the lanes that have it, then over the waves of the group
-  if constexpr (NT == 4) {
-    dskip[1] = nt % 2 ? dskip[0] : 0.0f;
-    dbias[1] = nt % 2 ? dbias[0] : 0.0f;
-    dskip[0] = nt % 2 ? 0.0f : dskip[0];
-    dbias[0] = nt % 2 ? 0.0f : dbias[0];
-  }
-  s_red[w][0][g][dl] = rows(halves(dskip[0], dskip[1]), halves(dbias[0], dbias[1]));
+  float4_t sums = s_dD[1][tid];
+  if (NT == 4) sums = nt % 2 ? (float4_t){0.0f, sums[0], 0.0f, sums[2]} : (float4_t){sums[0], 0.0f, sums[2], 0.0f};
+  s_red[w][0][g][dl] = rows(halves(sums[0], sums[1]), halves(sums[2], sums[3]));
   group_sync();
   if (nt == 0) {
     float s = 0.0f;

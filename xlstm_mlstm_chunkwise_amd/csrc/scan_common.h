@@ -20,6 +20,9 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // product, takes that out.  d = 0 gives 1.
 __device__ __forceinline__ float decay(float d, float A2) { return exp2_fast(fmaf(d, A2, 4e-9f)); }
 
+// The value is formed here, not behind what follows.
+__device__ __forceinline__ void formed(float& x) { asm volatile("" : "+v"(x)); }
+
 // 1 / (1 + e^-x)
 __device__ __forceinline__ float scan_sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + exp2_fast(-kLog2e * x));

@@ -33,8 +33,6 @@ typedef const float16_t __attribute__((address_space(4)))* uniform16_t;
 // The value is waited for here.
 __device__ __forceinline__ void arrived(float x) { asm volatile("" ::"s"(x)); }
 __device__ __forceinline__ void arrived_lane(float x) { asm volatile("" ::"v"(x)); }
-// The value is formed here, not behind what follows.
-__device__ __forceinline__ void formed(float& x) { asm volatile("" : "+v"(x)); }
 
 enum class Mode {
   kOutput,  // y and the final state
@@ -170,11 +168,11 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
   };
 
   // y of a tile whose parts of C . h are in LDS
-  auto finish = [&](int buf, int t, const own_t& x) {
+  auto finish = [&](int buf, int t, int end, const own_t& x) {
     own_t s = own(s_y[buf][0][0]);
 #pragma unroll
     for (int k = 1; k < kWaves; ++k) s += own(s_y[buf][k][0]);
-    const auto ay = vy.at(t + kOwn * w, t1);
+    const auto ay = vy.at(t + kOwn * w, end);
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
       float v = fmaf(skip, x[j], s[j]);
@@ -186,8 +184,10 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
 
   own_t x[2];  // of the tiles in the two buffers
   // A tile: its d and u are in buffer BUF, B and C of its first group on their way.
-  auto tile = [&](auto which, int t) {
+  // GRAD: it adds to the state gradient of its span.
+  auto tile = [&](auto which, auto back, int t) {
     constexpr int BUF = decltype(which)::value;
+    constexpr bool GRAD = decltype(back)::value;
     const bool more = t + kScanTile < t1;
     float4_t y;
     ask_quads(BUF, 0, 0);
@@ -220,13 +220,13 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
         const int k = j0 + j;
         const float dk = d4[set][k / 4][k % 4], uk = u4[set][k / 4][k % 4];
         float yk = 0.0f;
-        if (!ENTER || BACK) sum += dk;
+        if (!ENTER || GRAD) sum += dk;
 #pragma unroll
         for (int r = 0; r < NPW; ++r) {
           const float a = decay(dk, A2[r]);
           h[r] = fmaf(a, h[r], uk * B[j * NPW + r]);
           if (OUT) yk = r ? fmaf(C[j * NPW + r], h[r], yk) : C[j * NPW + r] * h[r];
-          if (BACK) {
+          if (GRAD) {
             W[r] *= a;
             G[r] = fmaf(C[j * NPW + r], W[r] * g4[set][k / 4][k % 4], G[r]);
           }
@@ -237,11 +237,12 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
 #pragma unroll
       for (int r = 0; r < NPW; ++r) {
         formed(h[r]);
-        if (BACK) formed(G[r]);
+        if (GRAD) formed(G[r]);
       }
       // the tile before, while the next group's operands come
       if (OUT && i == 0) {
-        if (t > t0) finish(BUF ^ 1, t - kScanTile, x[BUF ^ 1]);
+        // (in front of the first tile no row is inside)
+        finish(BUF ^ 1, t - kScanTile, t > t0 ? t1 : t - kScanTile, x[BUF ^ 1]);
         if (GATED) {
           const auto az = vz.at(t + kOwn * w, t1);
 #pragma unroll
@@ -261,10 +262,9 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
       if (in && w == 0) p.span_sums[i] = sum;
       sum = 0.0f;
     }
-    if (more) {
-      prepare(BUF ^ 1, t + kScanTile, x[BUF ^ 1]);
-      fetch(t + 2 * kScanTile);
-    }
+    // behind the last tile too: a branch would make the waits behind it the longer ones of both ways
+    prepare(BUF ^ 1, t + kScanTile, x[BUF ^ 1]);
+    fetch(t + 2 * kScanTile);
     __syncthreads();
   };
   if (t0 < t1) {
@@ -273,17 +273,24 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
     prepare(0, t0, x[0]);
     fetch(t0 + kScanTile);
     __syncthreads();
-    for (int t = t0;; t += 2 * kScanTile) {
-      tile(std::integral_constant<int, 0>{}, t);
+    typedef std::integral_constant<int, 0> even;
+    typedef std::integral_constant<int, 1> odd;
+    int t = t0;
+    if (BACK && t0 == 0) {
+      // nothing is in front of the first span (pairs of tiles) that would take its gradient
+      for (; t < p.span && t < t1; t += 2 * kScanTile) {
+        tile(even{}, std::false_type{}, t);
+        tile(odd{}, std::false_type{}, t + kScanTile);
+      }
+    }
+    for (; t < t1; t += 2 * kScanTile) {
+      tile(even{}, std::bool_constant<BACK>{}, t);
       if (t + kScanTile >= t1) {
-        if (OUT) finish(0, t, x[0]);
+        if (OUT) finish(0, t, t1, x[0]);
         break;
       }
-      tile(std::integral_constant<int, 1>{}, t + kScanTile);
-      if (t + 2 * kScanTile >= t1) {
-        if (OUT) finish(1, t + kScanTile, x[1]);
-        break;
-      }
+      tile(odd{}, std::bool_constant<BACK>{}, t + kScanTile);
+      if (OUT && t + 2 * kScanTile >= t1) finish(1, t + kScanTile, t1, x[1]);
     }
   }
   if (!in) return;
@@ -361,15 +368,18 @@ void scan_cut(ScanParams& p, bool back) {
     *length = (int)((tiles + n - 1) / n) * kScanTile;
     *pieces = *length ? (p.S + *length - 1) / *length : 1;
   };
-  // 512 workgroups are there at a time, two a compute unit
+  // 512 workgroups are there at a time, two a compute unit; one pass more over the
+  // states is paid for more of them (8 chunks of 64 workgroups 2.05 ms, 12 1.97, 16 2.06)
   const int64_t groups = (int64_t)p.B * ((p.D + kScanChannels - 1) / kScanChannels);
-  cut(groups <= 256 ? 512 / groups : 1, &p.chunks, &p.chunk);
+  cut(groups <= 256 ? 768 / groups : 1, &p.chunks, &p.chunk);
   p.spans = p.chunks;
   p.span = p.chunk;
   if (back) {
     const int ch = scan_back_channels(p.N);
     cut(512 / ((int64_t)p.B * ((p.D + ch - 1) / ch)), &p.spans, &p.span);
-    // whole spans in a chunk
+    // pairs of tiles in a span, whole spans in a chunk
+    p.span = (p.span + 2 * kScanTile - 1) / (2 * kScanTile) * (2 * kScanTile);
+    p.spans = p.span ? (p.S + p.span - 1) / p.span : 1;
     if (p.chunks > 1) {
       p.chunk = (p.chunk + p.span - 1) / p.span * p.span;
       p.chunks = (p.S + p.chunk - 1) / p.chunk;
