@@ -199,7 +199,8 @@ __global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams
       reinterpret_cast<float*>(&s_d[grp][q][dl])[k] = dlt;
       reinterpret_cast<float*>(&s_u[grp][q][dl])[k] = dlt * x;
       reinterpret_cast<float*>(&s_dr[grp][q][dl])[k] = dr;
-      s_item[r][tid] = (float4_t){x, scan_sigmoid(pre), dz, dr};
+      // (rows behind the last token have a gradient of d too, the one through A)
+      s_item[r][tid] = (float4_t){x, ok ? scan_sigmoid(pre) : 0.0f, dz, dr};
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
