@@ -1131,34 +1131,38 @@ def _normed(H, q, weight, bias, eps):
 # ---------------------------------------------------------------------------
 # views: (B, S, columns) tensors that may be a run of columns of a wider one
 
+_PLAIN = (0, 0)
+
+
 def _view(dev, name, t, shape, dtype):
     """Strides in elements of t from a sequence to the next and from a token to
-    the next (its last axis has to be adjacent), 0 where only one is there; for
-    (B, columns), one token, the first of them.  None passes."""
+    the next (its last axis has to be adjacent), 0 where only one is there or t
+    is contiguous; for (B, columns), one token, the first of them.  None passes."""
     if t is None:
-        return (0, 0)
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
+        return _PLAIN
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.is_contiguous():
-        return (0, 0)
-    strides, shape = t.stride(), t.shape
-    if shape[-1] > 1 and strides[-1] != 1:
+        return _PLAIN
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: its last axis must be adjacent in memory")
-    strides = tuple(0 if n <= 1 else s for s, n in zip(strides[:-1], shape[:-1]))
-    if any(s <= 0 and n > 1 for s, n in zip(strides, shape)) or 0 < strides[-1] < shape[-1]:
+    batch = strides[0] if shape[0] > 1 else 0
+    token = strides[1] if len(strides) == 3 and shape[1] > 1 else 0
+    if (batch <= 0 and shape[0] > 1) or (token <= 0 and len(strides) == 3 and shape[1] > 1) or 0 < token < shape[-1]:
         raise ValueError(f"{name} is broadcast or overlaps itself; make it contiguous")
-    return strides if len(strides) == 2 else (strides[0], 0)
+    return batch, token
 
 
 def _gpu_input(x, dims, layout):
     if x.dim() != dims:
         raise ValueError(f"x must be {layout}")
-    _out_code(x.dtype, "x")
     if not x.is_cuda:
+        _out_code(x.dtype, "x")
         raise ValueError("x must be a GPU tensor")
     return x.device
 
@@ -1220,8 +1224,8 @@ def causal_conv_fw(x, weight, bias=None, state=None, *, activation: Optional[str
     torch = _torch()
     dev, B, S, D, K, desc, _ = _conv_inputs("mlstm_conv_fw", x, weight, bias, state, activation)
     _check_on(dev, "y", out, (B, S, D), x.dtype)
-    y = torch.empty((B, S, D), dtype=x.dtype, device=dev) if out is None else out
-    state_out = torch.empty((B, K - 1, D), dtype=x.dtype, device=dev) if return_final_state else None
+    y = x.new_empty((B, S, D)) if out is None else out
+    state_out = x.new_empty((B, K - 1, D)) if return_final_state else None
     _call("mlstm_conv_fw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out))
     return y, state_out
 
@@ -1236,14 +1240,14 @@ def causal_conv_bw(x, weight, dy, bias=None, state=None, dstate=None, *, activat
     dev, B, S, D, K, desc, need = _conv_inputs("mlstm_conv_bw", x, weight, bias, state, activation)
     _check_on(dev, "dy", dy, (B, S, D), x.dtype)
     _check_on(dev, "dstate", dstate, (B, K - 1, D), x.dtype)
-    g = dict(dx=torch.empty((B, S, D), dtype=x.dtype, device=dev))
+    g = dict(dx=x.new_empty((B, S, D)))
     ws_bytes = 0
     if weight_grads:
         g["dw"] = torch.empty_like(weight)
-        g["db"] = torch.empty((D,), dtype=torch.float32, device=dev)
+        g["db"] = weight.new_empty((D,))
         workspace, ws_bytes = _bytes_of(need, workspace, dev)
     if state_grads:
-        g["dstate"] = torch.empty((B, K - 1, D), dtype=x.dtype, device=dev)
+        g["dstate"] = x.new_empty((B, K - 1, D))
     _call("mlstm_conv_bw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(dy), _ptr(dstate),
           _ptr(g["dx"]), _ptr(g.get("dstate")), _ptr(g.get("dw")), _ptr(g.get("db")),
           _ptr(workspace) if weight_grads else None, ws_bytes)
@@ -1265,9 +1269,9 @@ def causal_conv_step(x, weight, bias=None, state=None, *, activation: Optional[s
     _check_on(dev, "state", state, (B, K - 1, D), x.dtype)
     _check_on(dev, "state_out", state_out, (B, K - 1, D), x.dtype)
     desc, _ = _conv_plan("mlstm_conv_step", B, 1, D, K, x.dtype, activation, _view(dev, "x", x, x.shape, x.dtype))
-    y = torch.empty((B, D), dtype=x.dtype, device=dev)
+    y = x.new_empty((B, D))
     if state_out is None:
-        state_out = torch.empty((B, K - 1, D), dtype=x.dtype, device=dev)
+        state_out = x.new_empty((B, K - 1, D))
     _call("mlstm_conv_step", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out))
     return y, state_out
 
@@ -1344,22 +1348,26 @@ def _scan_plan(where, B, S, D, N, dtype, strides):
     return ctypes.byref(desc), scan_fw_workspace_bytes(desc), scan_bw_workspace_bytes(desc)
 
 
-def _scan_inputs(where, x, dt, A, B, C, D, z, dt_bias, h0):
+def _scan_inputs(where, dev, x, dt, A, B, C, D, z, dt_bias, h0):
     """Plan of the call and the sizes, checked; x is (B, S, D), or (B, D) for
     one token."""
     torch = _torch()
     if A.dim() != 2:
         raise ValueError("A must be (D, N)")
-    dev, dtype, rows, (ch, N) = x.device, x.dtype, tuple(x.shape[:-1]), A.shape
-    cols = rows + (N,)
-    _check_on(dev, "A", A, (x.shape[-1], N), torch.float32)
-    strides = (_view(dev, "x", x, x.shape, dtype), _view(dev, "dt", dt, x.shape, dtype),
-               _view(dev, "z", z, x.shape, dtype), _view(dev, "B", B, cols, dtype), _view(dev, "C", C, cols, dtype))
+    dtype, shape, N = x.dtype, x.shape, A.shape[1]
+    if len(shape) == 3:
+        nb, S, ch = shape
+        cols = (nb, S, N)
+    else:
+        (nb, ch), S = shape, 1
+        cols = (nb, N)
+    _check_on(dev, "A", A, (ch, N), torch.float32)
+    strides = (_view(dev, "x", x, shape, dtype), _view(dev, "dt", dt, shape, dtype), _view(dev, "z", z, shape, dtype),
+               _view(dev, "B", B, cols, dtype), _view(dev, "C", C, cols, dtype))
     _check_on(dev, "D", D, (ch,), torch.float32)
     _check_on(dev, "dt_bias", dt_bias, (ch,), torch.float32)
-    _check_on(dev, "h0", h0, (rows[0], ch, N), torch.float32)
-    S = rows[1] if len(rows) == 2 else 1
-    return dev, rows[0], S, ch, N, _scan_plan(where, rows[0], S, ch, N, dtype, strides)
+    _check_on(dev, "h0", h0, (nb, ch, N), torch.float32)
+    return nb, S, ch, N, _scan_plan(where, nb, S, ch, N, dtype, strides)
 
 
 def selective_scan_fw(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, out=None,
@@ -1377,11 +1385,11 @@ def selective_scan_fw(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, 
     state as it is, so rows of padding need that and finite x and B."""
     torch = _torch()
     dev = _gpu_input(x, 3, "(B, S, D)")
-    nb, S, ch, N, (desc, need, _) = _scan_inputs("mlstm_scan_fw", x, dt, A, B, C, D, z, dt_bias, h0)[1:]
+    nb, S, ch, N, (desc, need, _) = _scan_inputs("mlstm_scan_fw", dev, x, dt, A, B, C, D, z, dt_bias, h0)
     _check_on(dev, "y", out, (nb, S, ch), x.dtype)
     workspace, ws_bytes = _bytes_of(need, workspace, dev)
-    y = torch.empty((nb, S, ch), dtype=x.dtype, device=dev) if out is None else out
-    h = torch.empty((nb, ch, N), dtype=torch.float32, device=dev) if return_final_state else None
+    y = x.new_empty((nb, S, ch)) if out is None else out
+    h = A.new_empty((nb, ch, N)) if return_final_state else None
     _call("mlstm_scan_fw", dev, desc, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
           _ptr(h0), _ptr(y), _ptr(h), _ptr(workspace), ws_bytes)
     return y, h
@@ -1397,16 +1405,16 @@ def selective_scan_bw(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, h0=None,
     every eight tokens, and more), is allocated here unless it is given."""
     torch = _torch()
     dev = _gpu_input(x, 3, "(B, S, D)")
-    nb, S, ch, N, (desc, _, need) = _scan_inputs("mlstm_scan_bw", x, dt, A, B, C, D, z, dt_bias, h0)[1:]
+    nb, S, ch, N, (desc, _, need) = _scan_inputs("mlstm_scan_bw", dev, x, dt, A, B, C, D, z, dt_bias, h0)
     _check_on(dev, "dy", dy, (nb, S, ch), x.dtype)
     _check_on(dev, "dh", dh, (nb, ch, N), torch.float32)
     workspace, ws_bytes = _bytes_of(need, workspace, dev)
 
     def rows(n):
-        return torch.empty((nb, S, n), dtype=x.dtype, device=dev)
+        return x.new_empty((nb, S, n))
 
     def floats(*shape):
-        return torch.empty(shape, dtype=torch.float32, device=dev)
+        return A.new_empty(shape)
 
     g = dict(dx=rows(ch), ddt=rows(ch), dA=floats(ch, N), dB=rows(N), dC=rows(N), dD=floats(ch), dbias=floats(ch))
     if z is not None:
@@ -1425,11 +1433,11 @@ def selective_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, h=None, *,
     (y, h'); h_out may be h itself (updated in place)."""
     torch = _torch()
     dev = _gpu_input(x, 2, "(B, D)")
-    nb, _, ch, N, (desc, _, _) = _scan_inputs("mlstm_scan_step", x, dt, A, B, C, D, z, dt_bias, h)[1:]
+    nb, _, ch, N, (desc, _, _) = _scan_inputs("mlstm_scan_step", dev, x, dt, A, B, C, D, z, dt_bias, h)
     _check_on(dev, "h_out", h_out, (nb, ch, N), torch.float32)
-    y = torch.empty((nb, ch), dtype=x.dtype, device=dev)
+    y = x.new_empty((nb, ch))
     if h_out is None:
-        h_out = torch.empty((nb, ch, N), dtype=torch.float32, device=dev)
+        h_out = A.new_empty((nb, ch, N))
     _call("mlstm_scan_step", dev, desc, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
           _ptr(h), _ptr(y), _ptr(h_out))
     return y, h_out

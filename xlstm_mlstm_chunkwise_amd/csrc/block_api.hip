@@ -62,7 +62,7 @@ int validate(const mlstm_conv_desc_t* d) {
 }
 
 mlstm::ConvParams params(const mlstm_conv_desc_t* d, const void* x, const float* weight, const float* bias,
-                         const void* state) {
+                         const void* state, bool back) {
   mlstm::ConvParams p = {};
   p.x = view(x, d->x_strides, d->S, d->D);
   p.weight = weight;
@@ -74,7 +74,7 @@ mlstm::ConvParams params(const mlstm_conv_desc_t* d, const void* x, const float*
   p.K = d->K;
   p.bf16 = d->dtype == MLSTM_BF16;
   p.silu = d->silu;
-  mlstm::conv_runs(p.B, p.S, p.D, p.K, &p.run, &p.runs);
+  mlstm::conv_runs(p.B, p.S, p.D, p.K, back, &p.run, &p.runs);
   return p;
 }
 
@@ -169,7 +169,7 @@ int mlstm_conv_validate(const mlstm_conv_desc_t* desc) { return validate(desc); 
 
 size_t mlstm_conv_bw_workspace_bytes(const mlstm_conv_desc_t* desc) {
   if (validate(desc) != MLSTM_OK) return 0;
-  const mlstm::ConvParams p = params(desc, nullptr, nullptr, nullptr, nullptr);
+  const mlstm::ConvParams p = params(desc, nullptr, nullptr, nullptr, nullptr, true);
   return round_up((size_t)p.runs * (p.K + 1) * p.D * sizeof(float));
 }
 
@@ -180,7 +180,7 @@ int mlstm_conv_fw(const mlstm_conv_desc_t* desc, const void* x, const float* wei
   if (!weight || (desc->S > 0 && any_null({x, y}))) return MLSTM_E_NULLPTR;
   if ((st = check_aligned({x, state, y, state_out}, size_of(desc->dtype))) != MLSTM_OK) return st;
   if ((st = check_aligned({weight, bias}, 4)) != MLSTM_OK) return st;
-  mlstm::ConvParams p = params(desc, x, weight, bias, state);
+  mlstm::ConvParams p = params(desc, x, weight, bias, state, false);
   p.y = y;
   p.state_out = state_out;
   if (p.S == 0 && !state_out) return MLSTM_OK;
@@ -197,7 +197,7 @@ int mlstm_conv_bw(const mlstm_conv_desc_t* desc, const void* x, const float* wei
   if ((st = check_aligned({weight, bias, dweight, dbias}, 4)) != MLSTM_OK) return st;
   const bool sums = dweight || dbias;
   if (sums && !workspace_ok(workspace, workspace_bytes, mlstm_conv_bw_workspace_bytes(desc))) return MLSTM_E_WORKSPACE;
-  mlstm::ConvParams p = params(desc, x, weight, bias, state);
+  mlstm::ConvParams p = params(desc, x, weight, bias, state, true);
   p.dy = dy;
   p.dstate_out = dstate_out;
   p.dx = dx;
@@ -216,7 +216,7 @@ int mlstm_conv_step(const mlstm_conv_desc_t* desc, const void* x, const float* w
   if (any_null({x, weight, y, state_out})) return MLSTM_E_NULLPTR;
   if ((st = check_aligned({x, state, y, state_out}, size_of(desc->dtype))) != MLSTM_OK) return st;
   if ((st = check_aligned({weight, bias}, 4)) != MLSTM_OK) return st;
-  mlstm::ConvParams p = params(desc, x, weight, bias, state);
+  mlstm::ConvParams p = params(desc, x, weight, bias, state, false);
   p.y = y;
   p.state_out = state_out;
   return status(mlstm::launch_conv_step(p, static_cast<hipStream_t>(stream)));

@@ -2,9 +2,14 @@
 //   xe = [state, x];  p_t = bias + sum_k w_k xe_{t+k};  y_t = p_t sigmoid(p_t) or p_t
 //   g_t = dy_t (d y_t / d p_t);  dxe_j = sum_k w_k g_{j-k}
 //   dw_k = sum_t g_t xe_{t+k};   db = sum_t g_t
-// Everything is bound by memory: x is read and y written once, in 16-byte
-// pieces of adjacent channels, and the rows of the taps stay in registers.
-// The backward pass forms p again from the x that it reads anyhow.
+// Bound by memory: x is read and y written once, in pieces of adjacent channels,
+// and the rows of the taps stay in registers.  The backward pass forms p again
+// from the x that it reads anyhow.  8 sequences of 8192 x 4096, four taps, bf16:
+// forward 205 us for 1.07 GB (5.2 TB/s; threads of eight rows, which read three
+// rows and the weights again for each, 303 us), backward 334-356 us for 1.61 GB
+// (4.7 TB/s; about 32 vector instructions a value) and 7 us for the partial sums.
+#include <type_traits>
+
 #include "delta_common.h"
 #include "device_common.h"
 #include "kernels.h"
@@ -13,7 +18,6 @@ namespace mlstm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 8;  // rows of y a thread of the forward pass has
 
 // VEC adjacent channels as they are in memory.
 template <typename T, int VEC>
@@ -21,11 +25,15 @@ struct Piece {
   T v[VEC];
 };
 template <>
-struct Piece<bf16_t, 8> {
-  words4_t v;
+struct Piece<bf16_t, 4> {
+  words2_t v;
 };
 template <>
-struct Piece<bf16_t, 4> {
+struct Piece<bf16_t, 2> {
+  uint32_t v[1];
+};
+template <>
+struct Piece<float, 2> {
   words2_t v;
 };
 template <>
@@ -95,38 +103,59 @@ __device__ __forceinline__ Piece<T, VEC> row(const ConvParams& p, int b, int i, 
   return Piece<T, VEC>{};
 }
 
-// Thread: VEC channels of kRows rows of y.  Adjacent threads take adjacent
-// channels, then the next rows.
+// Thread: VEC channels of a run of rows of y, walked with the last K rows of xe
+// in registers and the next kAhead on their way.  Adjacent threads take adjacent
+// channels, then the next run.
+constexpr int kAhead = 4;
 template <typename T, int K, int VEC>
 __global__ __launch_bounds__(kThreads) void conv_kernel(const ConvParams p) {
-  const int nv = (p.D + VEC - 1) / VEC, nr = p.S > 0 ? (p.S + kRows - 1) / kRows : 1;
-  const int64_t n = (int64_t)nv * nr * p.B;
+  const int nv = (p.D + VEC - 1) / VEC, nr = p.runs / p.B;
+  const int64_t n = (int64_t)nv * p.runs;
   for (int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x; id < n; id += (int64_t)gridDim.x * kThreads) {
     const int64_t run = id / nv;
-    const int d = (int)(id - run * nv) * VEC, b = (int)(run / nr), r = (int)(run - (int64_t)b * nr), t0 = r * kRows;
-    Piece<T, VEC> raw[kRows + K - 1] = {};
+    const int d = (int)(id - run * nv) * VEC, b = (int)(run / nr), t0 = (int)(run - (int64_t)b * nr) * p.run;
+    const int t1 = min(t0 + p.run, p.S);
+    const T* px = static_cast<const T*>(p.x.p) + (size_t)b * p.x.batch + d;
+    T* py = static_cast<T*>(p.y) + (size_t)b * p.S * p.D + d;
+    Piece<T, VEC> raw[kAhead];
+    auto fetch = [&](int t) {  // behind the last row, the last again
 #pragma unroll
-    for (int i = 0; i < kRows + K - 1; ++i)
-      if (t0 + i < p.S + K - 1) raw[i] = row<T, K, VEC>(p, b, t0 + i, d);
-    float w[K][VEC], bias[VEC];
-    load_weights<K, VEC>(p, d, w, bias);
-    float x[kRows + K - 1][VEC];
+      for (int i = 0; i < kAhead; ++i)
+        raw[i] = *reinterpret_cast<const Piece<T, VEC>*>(px + (int64_t)min(t + i, t1 - 1) * p.x.token);
+    };
+    float w[K][VEC], bias[VEC], x[K][VEC];
+    if (t0 < t1) {
+      Piece<T, VEC> before[K - 1];
 #pragma unroll
-    for (int i = 0; i < kRows + K - 1; ++i) floats<T, VEC>(raw[i], x[i]);
+      for (int k = 0; k < K - 1; ++k) before[k] = row<T, K, VEC>(p, b, t0 + k, d);
+      fetch(t0);
+      load_weights<K, VEC>(p, d, w, bias);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (t0 + i >= p.S) break;
-      float y[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        float s = bias[e];
-#pragma unroll
-        for (int k = 0; k < K; ++k) s = fmaf(w[k][e], x[i + k][e], s);
-        y[e] = p.silu ? s * sigmoid(s) : s;
-      }
-      write<T, VEC>(p.y, ((size_t)b * p.S + t0 + i) * p.D + d, rounded<T, VEC>(y));
+      for (int k = 0; k < K - 1; ++k) floats<T, VEC>(before[k], x[k + 1]);
     }
-    if (r == nr - 1 && p.state_out)
+    for (int ta = t0; ta < t1; ta += kAhead) {
+      float nx[kAhead][VEC];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) floats<T, VEC>(raw[i], nx[i]);
+      fetch(ta + kAhead);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        float y[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) x[k][e] = x[k + 1][e];
+          x[K - 1][e] = nx[i][e];
+          float s = bias[e];
+#pragma unroll
+          for (int k = 0; k < K; ++k) s = fmaf(w[k][e], x[k][e], s);
+          y[e] = p.silu ? s * sigmoid(s) : s;
+        }
+        if (ta + i < t1)
+          *reinterpret_cast<Piece<T, VEC>*>(py + (size_t)(ta + i) * p.D) = rounded<T, VEC>(y);
+      }
+    }
+    if (t0 + p.run >= p.S && p.state_out)
       for (int i = 0; i < K - 1; ++i)
         write<T, VEC>(p.state_out, ((size_t)b * (K - 1) + i) * p.D + d, row<T, K, VEC>(p, b, p.S + i, d));
   }
@@ -162,95 +191,104 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(const ConvParams p)
   }
 }
 
-// Thread: VEC channels of a run of rows j of xe.  It walks up the run with the
-// last K rows of xe and the last K values of g in registers, beginning K - 1
-// rows below it for the g that reach into it; the next kAhead rows are on their
-// way meanwhile.
-constexpr int kAhead = 4;
+// Thread: VEC channels of a run of tokens.  It walks up the run and K - 1 rows
+// past it, whose g reach back into it, with the last K rows of xe and the last K
+// values of g in registers and the next kAhead rows on their way.  Row j of xe's
+// gradient is complete with g_j: token j - (K - 1), or a row of the state's.
 template <typename T, int K, int VEC>
 __global__ __launch_bounds__(kThreads) void conv_back_kernel(const ConvParams p) {
-  const int nv = (p.D + VEC - 1) / VEC, per = p.runs / p.B, last = p.S + K - 1;
+  const int nv = (p.D + VEC - 1) / VEC, per = p.runs / p.B;
   const int64_t n = (int64_t)nv * p.runs;
   for (int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x; id < n; id += (int64_t)gridDim.x * kThreads) {
     const int64_t run = id / nv;
-    const int d = (int)(id - run * nv) * VEC, b = (int)(run / per), j0 = (int)(run - (int64_t)b * per) * p.run;
-    const int j1 = min(j0 + p.run, last), first = max(j0 - (K - 1), 0);
-    float w[K][VEC], bias[VEC], dw[K][VEC] = {}, db[VEC] = {};
-    load_weights<K, VEC>(p, d, w, bias);
-    float x[K][VEC], g[K][VEC] = {};
-#pragma unroll
-    for (int k = 0; k < K - 1; ++k) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[k + 1][e] = 0.0f;
-      if (first + k < last) floats<T, VEC>(row<T, K, VEC>(p, b, first + k, d), x[k + 1]);
-    }
+    const int d = (int)(id - run * nv) * VEC, b = (int)(run / per), t0 = (int)(run - (int64_t)b * per) * p.run;
+    const int t1 = min(t0 + p.run, p.S), last = max(p.S - 1, 0);
+    const T* px = static_cast<const T*>(p.x.p) + (size_t)b * p.x.batch + d;
+    const T* py = static_cast<const T*>(p.dy) + (size_t)b * p.S * p.D + d;
+    T* pdx = static_cast<T*>(p.dx) + (size_t)b * p.S * p.D + d;
     Piece<T, VEC> rx[kAhead], ry[kAhead];
-    auto fetch = [&](int j) {
+    auto fetch = [&](int j) {  // behind the last row, the last again
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        rx[i] = ry[i] = Piece<T, VEC>{};
-        if (j + i < p.S && j + i < j1) {
-          rx[i] = row<T, K, VEC>(p, b, j + i + K - 1, d);
-          ry[i] = read<T, VEC>(p.dy, ((size_t)b * p.S + j + i) * p.D + d);
-        }
+        const int t = min(j + i, last);
+        rx[i] = *reinterpret_cast<const Piece<T, VEC>*>(px + (int64_t)t * p.x.token);
+        ry[i] = *reinterpret_cast<const Piece<T, VEC>*>(py + (size_t)t * p.D);
       }
     };
-    fetch(first);
-    for (int ja = first; ja < j1; ja += kAhead) {
-      float nx[kAhead][VEC], ny[kAhead][VEC];
+    float w[K][VEC], bias[VEC], dw[K][VEC] = {}, db[VEC] = {}, x[K][VEC] = {}, g[K][VEC] = {};
+    if (p.S > 0) {
+      Piece<T, VEC> before[K - 1];
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) before[k] = row<T, K, VEC>(p, b, t0 + k, d);
+      fetch(t0);
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) floats<T, VEC>(before[k], x[k + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) rx[i] = ry[i] = Piece<T, VEC>{};
+    }
+    load_weights<K, VEC>(p, d, w, bias);
+    // One row; EDGE: it may lie behind the run, or behind the sequence.
+    auto step = [&](auto edge, int j, const Piece<T, VEC>& nx, const Piece<T, VEC>& ny) {
+      constexpr bool EDGE = decltype(edge)::value;
+      float xn[VEC], yn[VEC], out[VEC];
+      floats<T, VEC>(nx, xn);
+      floats<T, VEC>(ny, yn);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) x[k][e] = x[k + 1][e];
+        x[K - 1][e] = xn[e];
+#pragma unroll
+        for (int k = K - 1; k > 0; --k) g[k][e] = g[k - 1][e];
+        float v = yn[e];
+        if (p.silu) {
+          float s = bias[e];
+#pragma unroll
+          for (int k = 0; k < K; ++k) s = fmaf(w[k][e], x[k][e], s);
+          const float sg = sigmoid(s);
+          v *= sg * fmaf(s, 1.0f - sg, 1.0f);
+        }
+        if (EDGE && j >= p.S) v = 0.0f;
+        g[0][e] = v;
+        if (EDGE && j >= t1) v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) dw[k][e] = EDGE && j >= t1 ? dw[k][e] : fmaf(v, x[k][e], dw[k][e]);
+        db[e] += v;
+        out[e] = w[0][e] * g[0][e];
+#pragma unroll
+        for (int k = 1; k < K; ++k) out[e] = fmaf(w[k][e], g[k][e], out[e]);
+      }
+      const int t = j - (K - 1);
+      if (EDGE && j >= p.S && p.dstate_out) {
+        float add[VEC];
+        floats<T, VEC>(read<T, VEC>(p.dstate_out, ((size_t)b * (K - 1) + j - p.S) * p.D + d), add);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] += add[e];
+      }
+      if (t >= t0)
+        *reinterpret_cast<Piece<T, VEC>*>(pdx + (size_t)t * p.D) = rounded<T, VEC>(out);
+      else if (t < 0 && p.dstate)
+        write<T, VEC>(p.dstate, ((size_t)b * (K - 1) + j) * p.D + d, rounded<T, VEC>(out));
+    };
+    int ja = t0;
+    for (; ja + kAhead <= t1; ja += kAhead) {
+      Piece<T, VEC> nx[kAhead], ny[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        floats<T, VEC>(rx[i], nx[i]);
-        floats<T, VEC>(ry[i], ny[i]);
+        nx[i] = rx[i];
+        ny[i] = ry[i];
       }
-      if (ja + kAhead < j1) fetch(ja + kAhead);
+      fetch(ja + kAhead);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int j = ja + i;
-        if (j >= j1) break;
-        float out[VEC];
+      for (int i = 0; i < kAhead; ++i) step(std::false_type{}, ja + i, nx[i], ny[i]);
+    }
+    // (at most 2 kAhead - 1 rows)
+    for (; ja < t1 + K - 1; ja += kAhead) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-          for (int k = 0; k < K - 1; ++k) x[k][e] = x[k + 1][e];
-          x[K - 1][e] = nx[i][e];
-#pragma unroll
-          for (int k = K - 1; k > 0; --k) g[k][e] = g[k - 1][e];
-          float dy = 0.0f;
-          if (j < p.S) {
-            dy = ny[i][e];
-            if (p.silu) {
-              float s = bias[e];
-#pragma unroll
-              for (int k = 0; k < K; ++k) s = fmaf(w[k][e], x[k][e], s);
-              const float sg = sigmoid(s);
-              dy *= sg * (1.0f + s * (1.0f - sg));
-            }
-          }
-          g[0][e] = dy;
-          out[e] = 0.0f;
-#pragma unroll
-          for (int k = 0; k < K; ++k) out[e] = fmaf(w[k][e], g[k][e], out[e]);
-        }
-        if (j < j0) continue;
-        if (j < p.S) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) dw[k][e] = fmaf(g[0][e], x[k][e], dw[k][e]);
-            db[e] += g[0][e];
-          }
-        } else if (p.dstate_out) {
-          float add[VEC];
-          floats<T, VEC>(read<T, VEC>(p.dstate_out, ((size_t)b * (K - 1) + j - p.S) * p.D + d), add);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) out[e] += add[e];
-        }
-        if (j >= K - 1)
-          write<T, VEC>(p.dx, ((size_t)b * p.S + j - (K - 1)) * p.D + d, rounded<T, VEC>(out));
-        else if (p.dstate)
-          write<T, VEC>(p.dstate, ((size_t)b * (K - 1) + j) * p.D + d, rounded<T, VEC>(out));
-      }
+      for (int i = 0; i < kAhead; ++i)
+        if (ja + i < t1 + K - 1) step(std::true_type{}, ja + i, rx[i], ry[i]);
+      if (ja + kAhead < t1 + K - 1 && p.S > 0) fetch(ja + kAhead);
     }
     if (p.partial) {
 #pragma unroll
@@ -308,9 +346,9 @@ unsigned groups_for(int64_t threads) {
 
 template <typename T, int K, int VEC>
 hipError_t launch(const ConvParams& p, Pass pass, hipStream_t stream) {
-  const int64_t nv = (p.D + VEC - 1) / VEC, nr = p.S > 0 ? (p.S + kRows - 1) / kRows : 1;
+  const int64_t nv = (p.D + VEC - 1) / VEC;
   if (pass == Pass::kForward)
-    hipLaunchKernelGGL((conv_kernel<T, K, VEC>), dim3(groups_for(nv * nr * p.B)), dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((conv_kernel<T, K, VEC>), dim3(groups_for(nv * p.runs)), dim3(kThreads), 0, stream, p);
   else if (pass == Pass::kBack)
     hipLaunchKernelGGL((conv_back_kernel<T, K, VEC>), dim3(groups_for(nv * p.runs)), dim3(kThreads), 0, stream, p);
   else
@@ -339,21 +377,28 @@ bool wide(const ConvParams& p) {
   return at % 16 == 0;
 }
 
+// Eight bytes a lane forward (8 sequences of 8192 x 4096 in bf16: 205 us, with
+// sixteen 206), four backward (334 us; eight, in twice the registers, 354, and
+// 13.9 against 17.4 at 3 of 1777 x 960); in float32 sixteen and eight bytes (8 of
+// 4096 x 4096 backward: 323 us, with sixteen 370).
 hipError_t launch_types(const ConvParams& p, Pass pass, hipStream_t stream) {
   if (!wide(p)) return p.bf16 ? launch_taps<bf16_t, 1>(p, pass, stream) : launch_taps<float, 1>(p, pass, stream);
-  if (!p.bf16) return launch_taps<float, 4>(p, pass, stream);
-  return pass == Pass::kBack ? launch_taps<bf16_t, 4>(p, pass, stream) : launch_taps<bf16_t, 8>(p, pass, stream);
+  if (pass == Pass::kBack) return p.bf16 ? launch_taps<bf16_t, 2>(p, pass, stream) : launch_taps<float, 2>(p, pass, stream);
+  return p.bf16 ? launch_taps<bf16_t, 4>(p, pass, stream) : launch_taps<float, 4>(p, pass, stream);
 }
 
 }  // namespace
 
-void conv_runs(int B, int S, int D, int K, int* run, int* runs) {
-  const int64_t lanes = (int64_t)B * ((D + 3) / 4), rows = (int64_t)S + K - 1;
-  int64_t per = (2048 * 64 + lanes - 1) / lanes, len = (rows + per - 1) / per;
-  if (len < 16) len = 16;
-  if (len > 512) len = 512;
+// Runs that leave kWaves waves of four channels a lane, of 16 rows at least and 512 at most.
+void conv_runs(int B, int S, int D, int K, bool back, int* run, int* runs) {
+  const int64_t lanes = (int64_t)B * ((D + 3) / 4), rows = S;
+  const int64_t waves = back ? 4096 : 8192, least = back ? 16 : 8, most = back ? 512 : 64;
+  int64_t per = (waves * 64 + lanes - 1) / lanes, len = (rows + per - 1) / per;
+  if (len < least) len = least;
+  if (len > most) len = most;
+  len = (len + kAhead - 1) / kAhead * kAhead;
   *run = (int)len;
-  *runs = (int)((rows + len - 1) / len) * B;
+  *runs = (int)(rows > 0 ? (rows + len - 1) / len : 1) * B;
 }
 
 hipError_t launch_conv(const ConvParams& p, hipStream_t stream) { return launch_types(p, Pass::kForward, stream); }

@@ -356,11 +356,11 @@ struct ConvParams {
   float* dbias;            // (D), may be null
   float* partial;          // (runs, K + 1, D), null when neither sum is wanted
   int B, S, D, K;
-  int runs, run;           // backward: runs of `run` rows of xe a sequence, `runs` in all
+  int runs, run;           // runs of `run` tokens, `runs` in all sequences together
   int bf16, silu;
 };
-// Rows a run of the backward pass has, and runs of all sequences together.
-void conv_runs(int B, int S, int D, int K, int* run, int* runs);
+// Rows a run has, and runs of all sequences together.
+void conv_runs(int B, int S, int D, int K, bool back, int* run, int* runs);
 hipError_t launch_conv(const ConvParams& p, hipStream_t stream);
 hipError_t launch_conv_back(const ConvParams& p, hipStream_t stream);
 hipError_t launch_conv_step(const ConvParams& p, hipStream_t stream);
