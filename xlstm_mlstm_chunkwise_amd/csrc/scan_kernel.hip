@@ -81,6 +81,7 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
   // lanes behind the last channel walk along with it and store nothing
   const uint32_t d = in ? db * kScanChannels + lane : p.D - 1;
   const int t0 = c * p.chunk, t1 = min(t0 + p.chunk, p.S);
+  const int grads = t0 ? t0 : p.span;  // kSpans: the first token whose gradient counts
   const float bias = p.bias ? p.bias[d] : 0.0f, skip = OUT && p.Dskip ? p.Dskip[d] : 0.0f;
 
   float A2[NPW], h[NPW], W[NPW], G[NPW];
@@ -115,18 +116,21 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) rdt[j] = Raw<T>::load(adt, vdt.off[j]);
     if (BACK) {
-      const auto ady = vdy.at(tq, t1);
+      // (not for tiles whose gradient is not asked for: no row is inside)
+      const int end = t >= grads ? t1 : t;
+      const auto ady = vdy.at(tq, end);
 #pragma unroll
       for (int j = 0; j < kOwn; ++j) rdy[j] = Raw<T>::load(ady, vdy.off[j]);
       if (GATED) {
-        const auto az = vz.at(tq, t1);
+        const auto az = vz.at(tq, end);
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) rz[j] = Raw<T>::load(az, vz.off[j]);
       }
     }
   };
   // Tokens behind the chunk's end have d = u = 0 and leave the state.
-  auto prepare = [&](int buf, int t, own_t& x) {
+  auto prepare = [&](auto back, int buf, int t, own_t& x) {
+    constexpr bool GRAD = decltype(back)::value;
     own_t dl, u, g;
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
@@ -134,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
       dl[j] = t + kOwn * w + j < t1 ? step : 0.0f;
       x[j] = Raw<T>::value(rx[j]);
       u[j] = dl[j] * x[j];
-      if (BACK) {
+      if (GRAD) {
         g[j] = Raw<T>::value(rdy[j]);
         const float z = GATED ? Raw<T>::value(rz[j]) : 0.0f;
         if (GATED) g[j] *= z * scan_sigmoid(z);
@@ -142,7 +146,7 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
     }
     own(s_d[buf][0]) = dl;
     own(s_u[buf][0]) = u;
-    if (BACK) own(s_g[buf][0]) = g;
+    if (GRAD) own(s_g[buf][0]) = g;
   };
 
   // B and C of a group of tokens, and d, u (and dr) of the next four or eight, are
@@ -153,17 +157,17 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
   constexpr int QG = GROUP > 4 ? GROUP / 4 : 1;  // quads a group has
   float16_t nB, nC;
   float4_t d4[2][QG], u4[2][QG], g4[2][QG];  // two sets in turn
-  auto ask = [&](int t, int i) {  // group i of the tile from t on
+  auto ask = [&](auto both, int t, int i) {  // group i of the tile from t on
     const uniform_t at = cols + (size_t)t * 2 * N + i * (32 * kWaves);
     nB = *(uniform16_t)at;
-    if (COLS) nC = *(uniform16_t)(at + 16);
+    if (decltype(both)::value) nC = *(uniform16_t)(at + 16);
   };
-  auto ask_quads = [&](int buf, int q, int set) {
+  auto ask_quads = [&](auto back, int buf, int q, int set) {
 #pragma unroll
     for (int k = 0; k < QG; ++k) {
       d4[set][k] = s_d[buf][q + k][lane];
       u4[set][k] = s_u[buf][q + k][lane];
-      if (BACK) g4[set][k] = s_g[buf][q + k][lane];
+      if (decltype(back)::value) g4[set][k] = s_g[buf][q + k][lane];
     }
   };
 
@@ -188,26 +192,31 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
   auto tile = [&](auto which, auto back, int t) {
     constexpr int BUF = decltype(which)::value;
     constexpr bool GRAD = decltype(back)::value;
+    // the tile behind an odd one may be the first whose gradient is asked for
+    constexpr bool NEXT = GRAD || (BACK && BUF == 1), READS = OUT || GRAD;
     const bool more = t + kScanTile < t1;
     float4_t y;
-    ask_quads(BUF, 0, 0);
+    ask_quads(back, BUF, 0, 0);
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i) {
       const int q = i * GROUP / 4, j0 = i * GROUP % 4, set = q / QG % 2;
       const float16_t B = nB, C = nC;
       arrived(B[0]);
-      if (COLS) arrived(C[0]);
+      if (READS) arrived(C[0]);
       if (j0 == 0) {
 #pragma unroll
         for (int k = 0; k < QG; ++k) {
           arrived_lane(d4[set][k][0]);
           arrived_lane(u4[set][k][0]);
-          if (BACK) arrived_lane(g4[set][k][0]);
+          if (GRAD) arrived_lane(g4[set][k][0]);
         }
-        if (q + QG < kQuads) ask_quads(BUF, q + QG, set ^ 1);
+        if (q + QG < kQuads) ask_quads(back, BUF, q + QG, set ^ 1);
       }
       // behind the last tile, the same tile again
-      ask(i + 1 < GROUPS || !more ? t : t + kScanTile, (i + 1) % GROUPS);
+      if (i + 1 < GROUPS)
+        ask(std::bool_constant<READS>{}, t, i + 1);
+      else
+        ask(std::bool_constant<OUT || NEXT>{}, more ? t + kScanTile : t, 0);
       __builtin_amdgcn_sched_barrier(0);
       if (KEEP && i * GROUP % kScanBlock == 0 && in) {
         const size_t block = (size_t)b * (p.rows / kScanBlock) + (t + i * GROUP) / kScanBlock;
@@ -263,14 +272,14 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(const ScanParams p) {
       sum = 0.0f;
     }
     // behind the last tile too: a branch would make the waits behind it the longer ones of both ways
-    prepare(BUF ^ 1, t + kScanTile, x[BUF ^ 1]);
+    prepare(std::bool_constant<NEXT>{}, BUF ^ 1, t + kScanTile, x[BUF ^ 1]);
     fetch(t + 2 * kScanTile);
     __syncthreads();
   };
   if (t0 < t1) {
     fetch(t0);
-    ask(t0, 0);
-    prepare(0, t0, x[0]);
+    ask(std::bool_constant<COLS>{}, t0, 0);
+    prepare(std::bool_constant<BACK>{}, 0, t0, x[0]);
     fetch(t0 + kScanTile);
     __syncthreads();
     typedef std::integral_constant<int, 0> even;
