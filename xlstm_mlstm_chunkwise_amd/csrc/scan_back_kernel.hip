@@ -335,7 +335,13 @@ __global__ __launch_bounds__(kThreads) void scan_back_columns_kernel(const ScanP
   const int groups = (p.D + scan_back_channels(p.N) - 1) / scan_back_channels(p.N);
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
     float s = 0.0f;
-    for (int k = 0; k < groups; ++k) s += p.part_bc[k * n + i];
+    for (int k = 0; k < groups; k += 8) {  // the loads of eight go out together
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = p.part_bc[min(k + j, groups - 1) * n + i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += k + j < groups ? x[j] : 0.0f;
+    }
     const int64_t row = i / (2 * p.N);
     const int col = (int)(i - row * 2 * p.N);
     IO* out = static_cast<IO*>(col < p.N ? p.dBm : p.dCm);
@@ -351,7 +357,13 @@ __global__ __launch_bounds__(kThreads) void scan_back_sums_kernel(const ScanPara
     float s = 0.0f;
     const float* from = i < na ? p.part_a + i : p.part_d + (i - na);
     const int64_t step = i < na ? na : 2 * p.D;
-    for (int k = 0; k < parts; ++k) s += from[k * step];
+    for (int k = 0; k < parts; k += 8) {  // the loads of eight go out together
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = from[min(k + j, parts - 1) * step];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += k + j < parts ? x[j] : 0.0f;
+    }
     if (i < na)
       p.dA[i] = s;
     else if (i < na + p.D) {

@@ -371,7 +371,7 @@ void scan_cut(ScanParams& p, bool back) {
   const int tiles = p.rows / kScanTile;
   // n pieces of whole tiles, four at least; every one has tokens
   auto cut = [&](int64_t n, int* pieces, int* length) {
-    if (n > tiles / 4) n = tiles / 4;
+    if (n > tiles / 2) n = tiles / 2;
     if (n > 64) n = 64;
     if (n < 1) n = 1;
     *length = (int)((tiles + n - 1) / n) * kScanTile;
