@@ -37,20 +37,36 @@ __device__ __forceinline__ float rows(float a, float b) {
   const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
-template <int CTRL>
-__device__ __forceinline__ float moved(float x) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
-}
 // Eight values summed over sixteen lanes: lane l of a row gets value l % 16 / 2.
-__device__ __forceinline__ float row_sums(const float (&v)[8], int l) {
-  float a[4], b[2];
-  const bool b3 = l & 8, b2 = l & 4, b1 = l & 2;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = (b3 ? v[i + 4] : v[i]) + moved<0x128>(b3 ? v[i] : v[i + 4]);  // rotated by eight
-#pragma unroll
-  for (int i = 0; i < 2; ++i) b[i] = (b2 ? a[i + 2] : a[i]) + moved<0x141>(b2 ? a[i] : a[i + 2]);  // half row mirrored
-  const float c = (b1 ? b[1] : b[0]) + moved<0x4E>(b1 ? b[0] : b[1]);                              // lane ^ 2
-  return c + moved<0xB1>(c);                                                                       // lane ^ 1
+// Each step adds a lane's partner and, in the half of the lanes that a bank mask
+// names, puts the sum of another value in its place: sixteen additions, where
+// selecting in front of them takes 22 instructions and waits between them.  A
+// lane move reads a register two instructions after its write at the earliest;
+// the order below keeps that, with the s_nop where it cannot.
+__device__ __forceinline__ float row_sums(float (&v)[8], uint64_t lanes_with_bit_1) {
+  float s;
+  asm("s_nop 1\n\t"
+      "v_add_f32_dpp %1, %1, %1 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %2, %2, %2 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %3, %3, %3 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %4, %4, %4 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %1, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %3, %7, %7 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %4, %8, %8 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %1, %1, %1 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %2, %2, %2 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %1, %3, %3 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %2, %4, %4 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %1, %1, %1 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %2, %2, %2 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_e64 %0, %1, %2, %9\n\t"
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %0, %0, %0 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf"
+      : "=&v"(s), "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])
+      : "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "s"(lanes_with_bit_1));
+  return s;
 }
 
 // The state gradient behind span `c`: the spans behind it, last to first.
@@ -252,7 +268,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_back_kernel(const ScanParams
         dA[i] = fmaf(de[k], wi, dA[i]);
         wa[k] = n ? fmaf(A2[i], wi, wa[k]) : A2[i] * wi;
       }
-      const float v1 = row_sums(v, lane);
+      const float v1 = row_sums(v, 0xCCCCCCCCCCCCCCCCull);
       if (lane % 2 == 0) s_part[buf][grp][t][(dl / 8) * N + n0 + dl / 2 % 4] = v1;
       s_red[w][t][g][dl] = rows(halves(s[0], s[1]), halves(wa[0], wa[1]));
       if (GATED) {
