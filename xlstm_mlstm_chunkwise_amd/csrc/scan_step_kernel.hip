@@ -1,5 +1,7 @@
 // Selective scan, one token, gfx950: the state is read and written once, in
 // pieces of four states a lane, and C . h is added over the lanes of a channel.
+// 8 sequences of 4096 channels of 16 states: 3.8 us, a launch's latency (4.7 MB:
+// 1 us).
 #include "scan_common.h"
 
 namespace mlstm {
