@@ -747,10 +747,11 @@ int mlstm_conv_step(const mlstm_conv_desc_t* desc,
  *   r_t[c]    = sum_n Cm_t[n] h_t[c, n] + Dskip[c] x_t[c]
  *   y_t[c]    = r_t[c] z_t[c] sigmoid(z_t[c])           (z given; else r_t[c])
  *
- * States, sums and products in float32.  dt = -inf leaves the state as it is
- * (d = 0) where x and Bm are finite.  A non-finite x, dt or z stays in its
- * channel (from its token on; in the backward pass dBm, dCm of the token have
- * it too); a non-finite Bm or Cm reaches every channel. */
+ * States, sums and products in float32.  A is finite.  dt = -inf leaves the
+ * state as it is (d = 0) where x and Bm are finite.  A non-finite x, dt, z or dy
+ * stays in its channel, from its token on (of the backward pass also in front of
+ * it), but for dBm and dCm of the tokens that it reaches there; a non-finite Bm
+ * or Cm reaches every channel. */
 typedef struct {
   int32_t B, S, D;     /* B, D >= 1, S >= 0; B * S * D below 2^40, S below
                           2^30, D below 2^22, B * ceil(D / 64) below 2^20     */
