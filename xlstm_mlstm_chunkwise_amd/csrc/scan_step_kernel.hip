@@ -21,11 +21,11 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(const ScanParams p)
     float4 h = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (p.h0) h = *reinterpret_cast<const float4*>(p.h0 + bd * N + n0);
     const float4 A = *reinterpret_cast<const float4*>(p.A + (size_t)d * N + n0);
-    const float x = at(p.x, d), dl = softplus(at(p.dt, d) + (p.bias ? p.bias[d] : 0.0f)), u = dl * x, s = kLog2e * dl;
-    h.x = fmaf(exp2_fast(s * A.x), h.x, u * at(p.Bm, n0));
-    h.y = fmaf(exp2_fast(s * A.y), h.y, u * at(p.Bm, n0 + 1));
-    h.z = fmaf(exp2_fast(s * A.z), h.z, u * at(p.Bm, n0 + 2));
-    h.w = fmaf(exp2_fast(s * A.w), h.w, u * at(p.Bm, n0 + 3));
+    const float x = at(p.x, d), dl = softplus(at(p.dt, d) + (p.bias ? p.bias[d] : 0.0f)), u = dl * x;
+    h.x = fmaf(decay(dl, kLog2e * A.x), h.x, u * at(p.Bm, n0));
+    h.y = fmaf(decay(dl, kLog2e * A.y), h.y, u * at(p.Bm, n0 + 1));
+    h.z = fmaf(decay(dl, kLog2e * A.z), h.z, u * at(p.Bm, n0 + 2));
+    h.w = fmaf(decay(dl, kLog2e * A.w), h.w, u * at(p.Bm, n0 + 3));
     *reinterpret_cast<float4*>(p.h_out + bd * N + n0) = h;
     float y = at(p.Cm, n0) * h.x + at(p.Cm, n0 + 1) * h.y + at(p.Cm, n0 + 2) * h.z + at(p.Cm, n0 + 3) * h.w;
 #pragma unroll
