@@ -71,7 +71,7 @@ __device__ __forceinline__ float row_sums(float (&v)[8], uint64_t lanes_with_bit
       "v_cndmask_b32_e64 %0, %1, %2, %9\n\t"
       "s_nop 1\n\t"
       "v_add_f32_dpp %0, %0, %0 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf"
-      : "=&v"(s), "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])
+      : "=&v"(s), "+&v"(v[0]), "+&v"(v[1]), "+&v"(v[2]), "+&v"(v[3])
       : "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "s"(lanes_with_bit_1));
   return s;
 }
