@@ -181,3 +181,19 @@ def test_refusals_on_the_gpu(mt):
         mt.causal_conv_fw(g["x"], g["w"], activation="gelu")
     with pytest.raises(mt.MlstmError):
         mt.causal_conv_fw(g["x"], torch.zeros(20, 5, device="cuda"))
+
+
+def test_outputs_apart_from_inputs(mt):
+    """out and state_out that share memory with what other threads read."""
+    store = torch.zeros(4 * 12 * 20, device="cuda")
+    x, w = store[:480].view(2, 12, 20), torch.ones(20, 4, device="cuda")
+    state = torch.zeros(3, 3, 20, device="cuda")
+    for out in (x, store[20:500].view(2, 12, 20), store[240:720].view(2, 12, 20)):
+        with pytest.raises(ValueError):
+            mt.causal_conv_fw(x, w, out=out)
+    out = store[480:].view(2, 12, 20)
+    assert mt.causal_conv_fw(x, w, out=out)[0] is out
+    with pytest.raises(ValueError):
+        mt.causal_conv_step(x[:, 0], w, None, state[:2], state_out=state[1:])
+    same = state[:2].view(2, 3, 20)
+    assert mt.causal_conv_step(x[:, 0], w, None, state[:2], state_out=same)[1] is same

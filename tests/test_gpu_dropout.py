@@ -138,3 +138,12 @@ def test_refusals_on_the_gpu(mt):
         with pytest.raises(TypeError):
             call()
     assert mt.dropout_fw(x[:0], 0.1, 1).shape == (0, 4)
+
+
+def test_out_in_place_or_apart(mt):
+    store = torch.ones(30, device="cuda")
+    for out, res in ((store[4:24], None), (store[10:], store[:20])):
+        with pytest.raises(ValueError):
+            mt.dropout_fw(store[:20], 0.5, 1, residual=res, out=out)
+    x = store[:20]
+    assert mt.dropout_fw(x, 0.5, 1, out=store[:20].view(20)).data_ptr() == x.data_ptr()

@@ -300,3 +300,20 @@ def test_refusals_on_the_gpu(mt):
         mt.selective_scan_fw(*_args(g), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         mt.selective_scan_bw(*_args(g)[:5], _dev(dy)[:, :5])
+
+
+def test_outputs_apart_from_inputs(mt):
+    """out and h_out that share memory with what other threads read."""
+    kw, _, _ = _draw(53, 2, 12, 20, 16, "f32")
+    g = _gpu(kw, "f32")
+    for out in (g["x"], g["dt"], g["z"]):
+        with pytest.raises(ValueError):
+            mt.selective_scan_fw(*_args(g), out=out)
+    out = torch.empty_like(g["x"])
+    assert mt.selective_scan_fw(*_args(g), out=out)[0] is out
+    h = torch.zeros(3, 20, 16, device="cuda")
+    x, dt, A, B, C = (v if v is g["A"] else v[:, 0] for v in _args(g)[:5])
+    with pytest.raises(ValueError):
+        mt.selective_scan_step(x, dt, A, B, C, h=h[:2], h_out=h[1:])
+    same = h[:2].view(2, 20, 16)
+    assert mt.selective_scan_step(x, dt, A, B, C, h=h[:2], h_out=same)[1] is same

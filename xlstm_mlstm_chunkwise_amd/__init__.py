@@ -1158,6 +1158,20 @@ def _view(dev, name, t, shape, dtype):
     return batch, token
 
 
+def _apart(name, out, same, *inputs):
+    """Refuses an `out` that shares memory with an input: other threads read it
+    after it is written.  `same`: out may be that input itself, value for value."""
+    start = out.data_ptr()
+    end = start + out.numel() * out.element_size()
+    for t in inputs:
+        if t is None or start == end or not t.numel() or (same and t.data_ptr() == start and t.is_contiguous()):
+            continue
+        first = t.data_ptr()
+        last = first + (sum((n - 1) * k for n, k in zip(t.shape, t.stride())) + 1) * t.element_size()
+        if first < end and start < last:
+            raise ValueError(f"{name} shares memory with an input")
+
+
 def _gpu_input(x, dims, layout):
     if x.dim() != dims:
         raise ValueError(f"x must be {layout}")
@@ -1220,10 +1234,13 @@ def causal_conv_fw(x, weight, bias=None, state=None, *, activation: Optional[str
     tensor; weight (D, K) float32, K 2 to 4, the last tap on the token itself;
     bias (D) float32 or None; state (B, K - 1, D) in x's dtype, the inputs in
     front of x, or None (zeros); activation None or "silu".  Returns (y, state'),
-    state' None when return_final_state is False."""
+    state' None when return_final_state is False.  out shares no memory with x or
+    state."""
     torch = _torch()
     dev, B, S, D, K, desc, _ = _conv_inputs("mlstm_conv_fw", x, weight, bias, state, activation)
-    _check_on(dev, "y", out, (B, S, D), x.dtype)
+    if out is not None:
+        _check_on(dev, "y", out, (B, S, D), x.dtype)
+        _apart("out", out, False, x, state)
     y = x.new_empty((B, S, D)) if out is None else out
     state_out = x.new_empty((B, K - 1, D)) if return_final_state else None
     _call("mlstm_conv_fw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out))
@@ -1277,6 +1294,9 @@ def causal_conv_step(x, weight, bias=None, state=None, *, activation: Optional[s
     y = x.new_empty((B, D))
     if state_out is None:
         state_out = x.new_empty((B, K - 1, D))
+    elif state_out is not state:
+        _apart("state_out", state_out, True, state)
+        _apart("state_out", state_out, False, x)
     _call("mlstm_conv_step", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out))
     return y, state_out
 
@@ -1315,7 +1335,8 @@ def _conv_function():
 def causal_conv(x, weight, bias=None, state=None, *, activation: Optional[str] = None, return_final_state: bool = False):
     """causal_conv_fw as a torch autograd function (gradients for x, weight,
     bias and state by mlstm_conv_bw).  Returns y, or (y, state') with
-    return_final_state; gradients flow in through both."""
+    return_final_state; gradients flow in through both.  A pass may be captured
+    into a graph as long as no eager graph of the same leaves is alive meanwhile."""
     return _conv_function().apply(x, weight, bias, state, activation, return_final_state)
 
 
@@ -1389,11 +1410,14 @@ def selective_scan_fw(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, 
     (no gate); A (D, N), D and dt_bias (D) or None (zeros), h0 (B, D, N) or None
     (zero state), float32.  Returns (y, h): y in x's dtype, h (B, D, N) float32,
     None when return_final_state is False.  A token with dt = -inf leaves the
-    state as it is, so rows of padding need that and finite x and B."""
+    state as it is, so rows of padding need that and finite x and B.  out shares
+    no memory with an input."""
     torch = _torch()
     dev = _gpu_input(x, 3, "(B, S, D)")
     nb, S, ch, N, (desc, need, _) = _scan_inputs("mlstm_scan_fw", dev, x, dt, A, B, C, D, z, dt_bias, h0)
-    _check_on(dev, "y", out, (nb, S, ch), x.dtype)
+    if out is not None:
+        _check_on(dev, "y", out, (nb, S, ch), x.dtype)
+        _apart("out", out, False, x, dt, z, B, C, h0)
     workspace, ws_bytes = _bytes_of(need, workspace, dev)
     y = x.new_empty((nb, S, ch)) if out is None else out
     h = A.new_empty((nb, ch, N)) if return_final_state else None
@@ -1445,6 +1469,9 @@ def selective_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, h=None, *,
     y = x.new_empty((nb, ch))
     if h_out is None:
         h_out = A.new_empty((nb, ch, N))
+    elif h_out is not h:
+        _apart("h_out", h_out, True, h)
+        _apart("h_out", h_out, False, x, dt, A, B, C, z)
     _call("mlstm_scan_step", dev, desc, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
           _ptr(h), _ptr(y), _ptr(h_out))
     return y, h_out
@@ -1527,7 +1554,9 @@ def dropout_fw(x, p: float, seed, offset: int = 0, *, residual=None, out=None):
     dev = x.device
     _check_on(dev, "x", x, x.shape, x.dtype)
     _check_on(dev, "residual", residual, x.shape, x.dtype)
-    _check_on(dev, "y", out, x.shape, x.dtype)
+    if out is not None:
+        _check_on(dev, "y", out, x.shape, x.dtype)
+        _apart("out", out, True, x, residual)
     seed_dev = None
     if isinstance(seed, torch.Tensor) and seed.is_cuda:
         _check_on(dev, "seed", seed, (2,), torch.int64)
@@ -1569,5 +1598,6 @@ def _dropout_function():
 
 def dropout(x, p: float, seed, offset: int = 0, *, residual=None):
     """dropout_fw as a torch autograd function: the gradient for x forms the
-    mask again, the one for residual is the incoming one."""
+    mask again, the one for residual is the incoming one.  A pass may be captured
+    into a graph as long as no eager graph of the same leaves is alive meanwhile."""
     return _dropout_function().apply(x, float(p), seed, offset, residual)
