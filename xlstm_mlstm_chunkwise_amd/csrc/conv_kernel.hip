@@ -379,9 +379,11 @@ bool wide(const ConvParams& p) {
 }
 
 // Eight bytes a lane forward (8 sequences of 8192 x 4096 in bf16: 205 us, with
-// sixteen 206), four backward (334 us; eight, in twice the registers, 354, and
-// 13.9 against 17.4 at 3 of 1777 x 960); in float32 sixteen and eight bytes (8 of
-// 4096 x 4096 backward: 323 us, with sixteen 370).
+// sixteen 206, with single channels, as rows at odd places need them, 272), four
+// backward (334 us; eight, in twice the registers, 354, and 13.9 against 17.4 at 3
+// of 1777 x 960; single channels 354 against 343 with the sums); in float32 sixteen
+// and eight bytes (8 of 4096 x 4096 backward: 323 us, with sixteen 370; 4 of 8192 x
+// 4096 forward 204 us, by single channels 214, backward 328 and 362).
 hipError_t launch_types(const ConvParams& p, Pass pass, hipStream_t stream) {
   if (!wide(p)) return p.bf16 ? launch_taps<bf16_t, 1>(p, pass, stream) : launch_taps<float, 1>(p, pass, stream);
   if (pass == Pass::kBack) return p.bf16 ? launch_taps<bf16_t, 2>(p, pass, stream) : launch_taps<float, 2>(p, pass, stream);
@@ -390,7 +392,14 @@ hipError_t launch_types(const ConvParams& p, Pass pass, hipStream_t stream) {
 
 }  // namespace
 
-// Runs that leave kWaves waves of four channels a lane, of 16 rows at least and 512 at most.
+// Runs that leave about 8192 waves of four channels a lane, of 8 rows at least and
+// 64 at most; backward 4096, 16 and 512, for every run leaves partial sums.  8
+// sequences of 8192 x 4096: forward 205 us in runs of 64 and of 32, 197 to 202 of
+// 128; backward with its sums 340 us with half the waves, 348 as here, 367 with
+// twice (the median of ten calls varies by 10 us from run to run).
+// 3 of 1777 x 960: forward 8.3 us in runs of 8, 9.2 of 4, 9.4 of 16; backward with
+// its sums 18.9 us in runs of 16, 21.2 of 8, 19.5 of 32; 1 of 256 x 64 forward 4.2
+// in runs of 8, 5.2 of 16.
 void conv_runs(int B, int S, int D, int K, bool back, int* run, int* runs) {
   const int64_t lanes = (int64_t)B * ((D + 3) / 4), rows = S;
   const int64_t waves = back ? 4096 : 8192, least = back ? 16 : 8, most = back ? 512 : 64;

@@ -19,9 +19,9 @@
 // Bound by vector issue: per state and token five slots form h again, nine walk
 // back, two to three are sums over lanes, and about 55 a token and channel stand
 // around them.  8 sequences of 8192 tokens, 4096 channels of 16 states, bf16: 2.84
-// ms in two spans (two waves a SIMD), 87 % of the cycles; with one span, one wave
-// a SIMD and more registers 6.5 ms at an earlier stage.  The sums over channels on
-// the matrix cores, by products with selectors, took 4.85 ms against 3.40.
+// ms in two spans (two waves a SIMD), 87 % of the cycles; in one span 4.0 ms.  The
+// sums over channels on the matrix cores, by products with selectors, took 4.85 ms
+// against 3.40.
 #include "scan_common.h"
 
 namespace mlstm {

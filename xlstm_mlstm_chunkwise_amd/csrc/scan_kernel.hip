@@ -393,6 +393,9 @@ void scan_cut(ScanParams& p, bool back) {
   p.spans = p.chunks;
   p.span = p.chunk;
   if (back) {
+    // 512 workgroups, two a compute unit (states and gradients of 8 sequences of
+    // 8192 tokens, 4096 channels of 16 states: 256 workgroups 0.97 + 4.00 ms, 512
+    // 1.33 + 2.81, 1024 1.49 + 2.78; of 3 of 1777, 960: 49 + 107, 48 + 81, 52 + 89 us)
     const int ch = scan_back_channels(p.N);
     cut(512 / ((int64_t)p.B * ((p.D + ch - 1) / ch)), &p.spans, &p.span);
     // pairs of tiles in a span, whole spans in a chunk
