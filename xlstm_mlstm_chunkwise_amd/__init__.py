@@ -1279,7 +1279,7 @@ def _conv_grads(dev, desc, need, x, weight, dy, bias, state, dstate, weight_grad
 def causal_conv_step(x, weight, bias=None, state=None, *, activation: Optional[str] = None, state_out=None):
     """One token of causal_conv_fw on the GPU (mlstm_conv_step): x (B, D), state
     (B, K - 1, D) or None (zeros).  Returns (y, state'); state_out may be state
-    itself (updated in place)."""
+    itself (updated in place); else it shares no memory with an input."""
     torch = _torch()
     dev = _gpu_input(x, 2, "(B, D)")
     B, D = x.shape
@@ -1294,9 +1294,8 @@ def causal_conv_step(x, weight, bias=None, state=None, *, activation: Optional[s
     y = x.new_empty((B, D))
     if state_out is None:
         state_out = x.new_empty((B, K - 1, D))
-    elif state_out is not state:
-        _apart("state_out", state_out, True, state)
-        _apart("state_out", state_out, False, x)
+    elif state is not None and 0 < abs(state_out.data_ptr() - state.data_ptr()) < state.nbytes:
+        raise ValueError("state_out is neither state itself nor apart from it")
     _call("mlstm_conv_step", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out))
     return y, state_out
 
@@ -1461,7 +1460,8 @@ def _scan_grads(dev, desc, need, x, dt, A, B, C, dy, D, z, dt_bias, h0, dh, stat
 def selective_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, h=None, *, h_out=None):
     """One token of selective_scan_fw on the GPU (mlstm_scan_step): x, dt, z
     (B, D), B, C (B, N), h (B, D, N) float32 or None (zero state).  Returns
-    (y, h'); h_out may be h itself (updated in place)."""
+    (y, h'); h_out may be h itself (updated in place); else it shares no memory
+    with an input."""
     torch = _torch()
     dev = _gpu_input(x, 2, "(B, D)")
     nb, _, ch, N, (desc, _, _) = _scan_inputs("mlstm_scan_step", dev, x, dt, A, B, C, D, z, dt_bias, h)
@@ -1469,9 +1469,8 @@ def selective_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, h=None, *,
     y = x.new_empty((nb, ch))
     if h_out is None:
         h_out = A.new_empty((nb, ch, N))
-    elif h_out is not h:
-        _apart("h_out", h_out, True, h)
-        _apart("h_out", h_out, False, x, dt, A, B, C, z)
+    elif h is not None and 0 < abs(h_out.data_ptr() - h.data_ptr()) < h.nbytes:
+        raise ValueError("h_out is neither h itself nor apart from it")
     _call("mlstm_scan_step", dev, desc, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
           _ptr(h), _ptr(y), _ptr(h_out))
     return y, h_out
