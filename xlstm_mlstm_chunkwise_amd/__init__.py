@@ -1256,20 +1256,14 @@ def causal_conv_bw(x, weight, dy, bias=None, state=None, dstate=None, *, activat
     dev, B, S, D, K, desc, need = _conv_inputs("mlstm_conv_bw", x, weight, bias, state, activation)
     _check_on(dev, "dy", dy, (B, S, D), x.dtype)
     _check_on(dev, "dstate", dstate, (B, K - 1, D), x.dtype)
-    return _conv_grads(dev, desc, need, x, weight, dy, bias, state, dstate, weight_grads, state_grads, workspace)
-
-
-def _conv_grads(dev, desc, need, x, weight, dy, bias, state, dstate, weight_grads, state_grads, workspace=None):
-    """causal_conv_bw for checked inputs."""
-    D, K = weight.shape
-    g = dict(dx=x.new_empty(x.shape))
+    g = dict(dx=x.new_empty((B, S, D)))
     ws_bytes = 0
     if weight_grads:
         g["dw"] = weight.new_empty((D, K))
         g["db"] = weight.new_empty((D,))
         workspace, ws_bytes = _bytes_of(need, workspace, dev)
     if state_grads:
-        g["dstate"] = x.new_empty((x.shape[0], K - 1, D))
+        g["dstate"] = x.new_empty((B, K - 1, D))
     _call("mlstm_conv_bw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(dy), _ptr(dstate),
           _ptr(g["dx"]), _ptr(g.get("dstate")), _ptr(g.get("dw")), _ptr(g.get("db")),
           _ptr(workspace) if weight_grads else None, ws_bytes)
@@ -1310,9 +1304,7 @@ def _conv_function():
                 y, s = causal_conv_fw(x, weight, bias, state, activation=activation, return_final_state=final_state)
                 ctx.save_for_backward(x, weight, bias, state)
                 ctx.set_materialize_grads(False)
-                # the saved tensors are what the forward has checked, and dy has y's shape and type
-                dev, _, _, _, _, desc, need = _conv_inputs("mlstm_conv_bw", x, weight, bias, state, activation)
-                ctx.plan = dev, desc, need
+                ctx.activation = activation
                 return (y, s) if final_state else y
 
             @staticmethod
@@ -1323,8 +1315,9 @@ def _conv_function():
                     return (None,) * 6
                 dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _readable(dy)
                 need = ctx.needs_input_grad
-                g = _conv_grads(*ctx.plan, x, weight, dy, bias, state, None if ds is None else _readable(ds),
-                                need[1] or need[2], need[3])
+                # checked again: a hook may hand back a saved tensor with other strides, or as another one
+                g = causal_conv_bw(x, weight, dy, bias, state, None if ds is None else _readable(ds), activation=ctx.activation,
+                                   weight_grads=need[1] or need[2], state_grads=need[3])
                 return (g["dx"], g.get("dw"), g.get("db") if bias is not None else None, g.get("dstate"), None, None)
 
         _functions["conv"] = CausalConv
@@ -1438,19 +1431,14 @@ def selective_scan_bw(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, h0=None,
     nb, S, ch, N, (desc, _, need) = _scan_inputs("mlstm_scan_bw", dev, x, dt, A, B, C, D, z, dt_bias, h0)
     _check_on(dev, "dy", dy, (nb, S, ch), x.dtype)
     _check_on(dev, "dh", dh, (nb, ch, N), torch.float32)
-    return _scan_grads(dev, desc, need, x, dt, A, B, C, dy, D, z, dt_bias, h0, dh, state_grads, workspace)
-
-
-def _scan_grads(dev, desc, need, x, dt, A, B, C, dy, D, z, dt_bias, h0, dh, state_grads, workspace=None):
-    """selective_scan_bw for checked inputs."""
-    shape, (ch, N), row = x.shape, A.shape, A.new_empty
+    shape, row = (nb, S, ch), A.new_empty
     workspace, ws_bytes = _bytes_of(need, workspace, dev)
     g = dict(dx=x.new_empty(shape), ddt=x.new_empty(shape), dA=row((ch, N)), dB=x.new_empty(B.shape), dC=x.new_empty(B.shape),
              dD=row((ch,)), dbias=row((ch,)))
     if z is not None:
         g["dz"] = x.new_empty(shape)
     if state_grads:
-        g["dh0"] = row((shape[0], ch, N))
+        g["dh0"] = row((nb, ch, N))
     _call("mlstm_scan_bw", dev, desc, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
           _ptr(h0), _ptr(dy), _ptr(dh), _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]),
           _ptr(g["dD"]), _ptr(g.get("dz")), _ptr(g["dbias"]), _ptr(g.get("dh0")), _ptr(workspace), ws_bytes)
@@ -1486,9 +1474,6 @@ def _scan_function():
                 y, h = selective_scan_fw(x, dt, A, B, C, D, z, dt_bias, h0, return_final_state=final_state)
                 ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, h0)
                 ctx.set_materialize_grads(False)
-                # the saved tensors are what the forward has checked, and dy has y's shape and type
-                _, _, _, _, (desc, _, need) = _scan_inputs("mlstm_scan_bw", x.device, x, dt, A, B, C, D, z, dt_bias, h0)
-                ctx.plan = x.device, desc, need
                 return (y, h) if final_state else y
 
             @staticmethod
@@ -1498,8 +1483,9 @@ def _scan_function():
                 if dy is None and dh is None:
                     return (None,) * 10
                 dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _readable(dy)
-                g = _scan_grads(*ctx.plan, x, dt, A, B, C, dy, D, z, dt_bias, h0, None if dh is None else _readable(dh),
-                                ctx.needs_input_grad[8])
+                # checked again: a hook may hand back a saved tensor with other strides, or as another one
+                g = selective_scan_bw(x, dt, A, B, C, dy, D, z, dt_bias, h0, None if dh is None else _readable(dh),
+                                      state_grads=ctx.needs_input_grad[8])
                 return (g["dx"], g["ddt"], g["dA"], g["dB"], g["dC"], None if D is None else g["dD"], g.get("dz"),
                         None if dt_bias is None else g["dbias"], g.get("dh0"), None)
 
