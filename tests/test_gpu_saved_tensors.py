@@ -82,3 +82,19 @@ def test_dropout_with_its_seed_on_the_device(mt, hook):
     with HOOKS[hook]():
         back = grads()
     assert all(torch.equal(g, w) for g, w in zip(back(), want))
+
+
+@pytest.mark.parametrize("hook", list(HOOKS))
+def test_head_norm(mt, hook):
+    n = _normal(4)
+    x, w, b = n(2, 3, 20, 64).requires_grad_(True), n(3, 64).requires_grad_(True), n(3, 64).requires_grad_(True)
+    dy = n(2, 20, 3, 64)
+
+    def grads():
+        y = mt.head_norm(x, w, b)
+        return lambda: torch.autograd.grad(y, [x, w, b], dy)
+
+    want = grads()()
+    with HOOKS[hook]():
+        back = grads()
+    assert all(torch.equal(g, r) for g, r in zip(back(), want))

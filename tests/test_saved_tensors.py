@@ -99,3 +99,26 @@ def test_other_types_and_shapes_are_refused(calls, change):
         with pytest.raises((TypeError, ValueError, IndexError)):
             torch.autograd.grad(y, [x], torch.randn(B, S, D))
     assert len(calls) == 2
+
+
+def test_head_norm(calls, monkeypatch):
+    """A weight of another type or shape, x as a transposed copy."""
+    x, w = torch.randn(2, 3, 5, 64, requires_grad=True), torch.randn(3, 64, requires_grad=True)
+
+    def inputs(x):
+        if not x.is_contiguous():
+            raise ValueError("x must be contiguous")
+        return x.shape
+
+    monkeypatch.setattr(mt, "_norm_input", inputs)
+    for change in (lambda t: t.to(torch.bfloat16) if t.dim() == 2 else t, lambda t: t[:1] if t.dim() == 2 else t,
+                   lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)):
+        with _Kept(change).hooks():
+            y = mt.head_norm(x, w)
+        with pytest.raises((TypeError, ValueError)):
+            torch.autograd.grad(y, [x, w], torch.randn_like(y))
+    assert [where for where, _ in calls] == ["mlstm_head_norm_fw"] * 3
+    calls.clear()
+    y = mt.head_norm(x, w)
+    torch.autograd.grad(y, [x, w], torch.randn_like(y))
+    assert [where for where, _ in calls] == ["mlstm_head_norm_fw", "mlstm_head_norm_bw"]

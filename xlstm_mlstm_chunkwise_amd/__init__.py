@@ -1062,19 +1062,16 @@ def head_norm_bw(x, dy, weight=None, *, eps: float = 1e-6, weight_grads: bool = 
     """Backward pass of head_norm_fw on the GPU (mlstm_head_norm_bw): (dx,
     dweight, dbias) from x, dy (B, S, NH, D) and the weight; dx in x's dtype,
     dweight and dbias (NH, D) float32, None without weight_grads."""
+    return _norm_grads(x, dy, weight, eps, weight_grads, weight_grads, workspace)
+
+
+def _norm_grads(x, dy, weight, eps, weight_grad, bias_grad, workspace=None):
+    """head_norm_bw with either of the two sums left out."""
     torch = _torch()
     B, NH, S, D = _norm_input(x)
     dev = x.device
     _check_on(dev, "dy", dy, (B, S, NH, D), dy.dtype)
     _check_on(dev, "weight", weight, (NH, D), torch.float32)
-    return _norm_grads(x, dy, weight, eps, weight_grads, weight_grads, workspace)
-
-
-def _norm_grads(x, dy, weight, eps, weight_grad, bias_grad, workspace=None):
-    """head_norm_bw for checked inputs, with either of the two sums left out."""
-    torch = _torch()
-    B, NH, S, D = x.shape
-    dev = x.device
     desc, need = _norm_plan("mlstm_head_norm_bw", B, NH, S, D, x.dtype, dy.dtype, float(eps))
     dx, ws_bytes = torch.empty_like(x), 0
 
@@ -1107,7 +1104,7 @@ def _head_norm_function():
             def backward(ctx, dy):
                 x, weight = ctx.saved_tensors
                 _, need_w, need_b, _, _ = ctx.needs_input_grad
-                # the forward has checked x and weight, and dy has y's shape and type
+                # (x and weight are checked again: a hook may hand back a saved tensor as another one)
                 return (*_norm_grads(x, _readable(dy), weight, ctx.eps, need_w, need_b), None, None)
 
         _functions["norm"] = HeadNorm
