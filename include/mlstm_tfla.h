@@ -75,7 +75,8 @@ typedef enum {
   MLSTM_E_WORKSPACE = 6,   /* workspace missing or smaller than required       */
   MLSTM_E_HIP = 7,         /* a HIP launch or runtime call failed              */
   MLSTM_E_ALIGN = 8,       /* a pointer violates its alignment requirement     */
-  MLSTM_E_ARG = 9          /* other invalid argument (gate, precision, eps...) */
+  MLSTM_E_ARG = 9,         /* other invalid argument (gate, precision, eps...) */
+  MLSTM_E_OVERLAP = 10     /* an output shares memory with an input            */
 } mlstm_status_t;
 
 typedef enum { MLSTM_F32 = 0, MLSTM_BF16 = 1 } mlstm_dtype_t;
@@ -686,6 +687,11 @@ int mlstm_head_norm_bw(const mlstm_head_norm_desc_t* desc,
  * next; 0 stands for the stride of a contiguous tensor.  The token's stride is
  * at least the number of columns (tokens do not overlap) and below 2^25.  Such
  * inputs need the alignment of one element only.  Everything else is contiguous.
+ *
+ * Outputs share no memory with inputs, but for what is said below of states and
+ * dropout in place: other threads still read what one has written.  An output
+ * that begins or ends between an input's first and last byte (a view's gaps
+ * between rows among them) is refused with MLSTM_E_OVERLAP.
  *
  * Short causal convolution, every channel by itself, K taps:
  *

@@ -35,7 +35,7 @@ _CODES = {"split": MLSTM_STATES_SPLIT, "int16": MLSTM_STATES_I16}
 STATUS_NAMES = {
     0: "MLSTM_OK", 1: "MLSTM_E_NULLPTR", 2: "MLSTM_E_SHAPE", 3: "MLSTM_E_CHUNK",
     4: "MLSTM_E_DTYPE", 5: "MLSTM_E_UNSUPPORTED", 6: "MLSTM_E_WORKSPACE",
-    7: "MLSTM_E_HIP", 8: "MLSTM_E_ALIGN", 9: "MLSTM_E_ARG",
+    7: "MLSTM_E_HIP", 8: "MLSTM_E_ALIGN", 9: "MLSTM_E_ARG", 10: "MLSTM_E_OVERLAP",
 }
 
 
@@ -43,6 +43,10 @@ class MlstmError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)} ({status_str(status)})")
+
+
+class OverlapError(MlstmError, ValueError):
+    """An output that the caller gave shares memory with an input."""
 
 
 class FwDesc(ctypes.Structure):
@@ -800,7 +804,8 @@ def _check_on(dev, name, t, shape, dtype):
 
 def _call(where, dev, *args):
     """Run a C entry point on dev's current stream (appended as the last
-    argument); raises MlstmError for a non-zero status."""
+    argument); raises MlstmError for a non-zero status, OverlapError for an output
+    that shares memory with an input."""
     torch = _torch()
     fn, index = getattr(lib(), where), dev.index
     stream = torch._C._cuda_getCurrentRawStream(index)
@@ -810,7 +815,7 @@ def _call(where, dev, *args):
         with torch.cuda.device(index):
             st = fn(*args, stream)
     if st:
-        raise MlstmError(st, where)
+        raise (OverlapError if st == 10 else MlstmError)(st, where)
 
 
 def _bytes_of(need, workspace, dev):
@@ -1155,20 +1160,6 @@ def _view(dev, name, t, shape, dtype):
     return batch, token
 
 
-def _apart(name, out, same, *inputs):
-    """Refuses an `out` that shares memory with an input: other threads read it
-    after it is written.  `same`: out may be that input itself, value for value."""
-    start = out.data_ptr()
-    end = start + out.numel() * out.element_size()
-    for t in inputs:
-        if t is None or start == end or not t.numel() or (same and t.data_ptr() == start and t.is_contiguous()):
-            continue
-        first = t.data_ptr()
-        last = first + (sum((n - 1) * k for n, k in zip(t.shape, t.stride())) + 1) * t.element_size()
-        if first < end and start < last:
-            raise ValueError(f"{name} shares memory with an input")
-
-
 def _gpu_input(x, dims, layout):
     if x.dim() != dims:
         raise ValueError(f"x must be {layout}")
@@ -1231,13 +1222,12 @@ def causal_conv_fw(x, weight, bias=None, state=None, *, activation: Optional[str
     tensor; weight (D, K) float32, K 2 to 4, the last tap on the token itself;
     bias (D) float32 or None; state (B, K - 1, D) in x's dtype, the inputs in
     front of x, or None (zeros); activation None or "silu".  Returns (y, state'),
-    state' None when return_final_state is False.  out shares no memory with x or
-    state."""
+    state' None when return_final_state is False.  out shares no memory with an
+    input."""
     torch = _torch()
     dev, B, S, D, K, desc, _ = _conv_inputs("mlstm_conv_fw", x, weight, bias, state, activation)
     if out is not None:
         _check_on(dev, "y", out, (B, S, D), x.dtype)
-        _apart("out", out, False, x, state)
     y = x.new_empty((B, S, D)) if out is None else out
     state_out = x.new_empty((B, K - 1, D)) if return_final_state else None
     _call("mlstm_conv_fw", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out))
@@ -1285,8 +1275,6 @@ def causal_conv_step(x, weight, bias=None, state=None, *, activation: Optional[s
     y = x.new_empty((B, D))
     if state_out is None:
         state_out = x.new_empty((B, K - 1, D))
-    elif state is not None and 0 < abs(state_out.data_ptr() - state.data_ptr()) < state.nbytes:
-        raise ValueError("state_out is neither state itself nor apart from it")
     _call("mlstm_conv_step", dev, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out))
     return y, state_out
 
@@ -1406,7 +1394,6 @@ def selective_scan_fw(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, 
     nb, S, ch, N, (desc, need, _) = _scan_inputs("mlstm_scan_fw", dev, x, dt, A, B, C, D, z, dt_bias, h0)
     if out is not None:
         _check_on(dev, "y", out, (nb, S, ch), x.dtype)
-        _apart("out", out, False, x, dt, z, B, C, h0)
     workspace, ws_bytes = _bytes_of(need, workspace, dev)
     y = x.new_empty((nb, S, ch)) if out is None else out
     h = A.new_empty((nb, ch, N)) if return_final_state else None
@@ -1454,8 +1441,6 @@ def selective_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, h=None, *,
     y = x.new_empty((nb, ch))
     if h_out is None:
         h_out = A.new_empty((nb, ch, N))
-    elif h is not None and 0 < abs(h_out.data_ptr() - h.data_ptr()) < h.nbytes:
-        raise ValueError("h_out is neither h itself nor apart from it")
     _call("mlstm_scan_step", dev, desc, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
           _ptr(h), _ptr(y), _ptr(h_out))
     return y, h_out
@@ -1538,7 +1523,6 @@ def dropout_fw(x, p: float, seed, offset: int = 0, *, residual=None, out=None):
     _check_on(dev, "residual", residual, x.shape, x.dtype)
     if out is not None:
         _check_on(dev, "y", out, x.shape, x.dtype)
-        _apart("out", out, True, x, residual)
     seed_dev = None
     if isinstance(seed, torch.Tensor) and seed.is_cuda:
         _check_on(dev, "seed", seed, (2,), torch.int64)

@@ -580,6 +580,7 @@ const char* mlstm_status_str(int status) {
     case MLSTM_E_HIP: return "HIP launch failed";
     case MLSTM_E_ALIGN: return "misaligned pointer";
     case MLSTM_E_ARG: return "invalid argument";
+    case MLSTM_E_OVERLAP: return "output shares memory with an input";
     default: return "unknown status";
   }
 }

@@ -2,6 +2,7 @@
 // argument validation, workspace layout and launches.  See
 // include/mlstm_tfla.h for the contract of every entry point.
 #include <math.h>
+#include <array>
 #include <initializer_list>
 #include <stdint.h>
 
@@ -30,6 +31,31 @@ int status(hipError_t e) { return e == hipSuccess ? MLSTM_OK : MLSTM_E_HIP; }
 bool workspace_ok(const void* ws, size_t bytes, size_t need) {
   return need == 0 || (ws && bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255) == 0);
 }
+
+// A tensor's memory, from its first byte to behind its last; empty if it is not given.
+struct Span {
+  uintptr_t first, end;
+};
+
+Span span(const void* p, int64_t bytes) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return {at, p ? at + (uintptr_t)bytes : at};
+}
+
+Span span(const mlstm::View& v, int64_t B, int64_t S, int64_t columns, int64_t size) {
+  return span(v.p, S ? ((B - 1) * v.batch + (S - 1) * v.token + columns) * size : 0);
+}
+
+// Whether an output shares memory with an input: other threads read that after
+// it is written.
+template <typename Ins>
+int check_apart(std::initializer_list<Span> outs, const Ins& ins) {
+  for (const Span& o : outs)
+    for (const Span& i : ins)
+      if (o.first < o.end && i.first < i.end && o.first < i.end && i.first < o.end) return MLSTM_E_OVERLAP;
+  return MLSTM_OK;
+}
+typedef std::initializer_list<Span> Spans;
 
 // 0 stands for a contiguous tensor's strides.
 mlstm::View view(const void* p, const int64_t (&strides)[2], int64_t S, int64_t columns) {
@@ -78,6 +104,20 @@ mlstm::ConvParams params(const mlstm_conv_desc_t* d, const void* x, const float*
   return p;
 }
 
+// The inputs' memory but the state's, and the bytes of x's rows, the state and the weights.
+struct ConvSpans {
+  int64_t rows, state, weight, bias;
+  std::array<Span, 3> in;
+  ConvSpans(const mlstm_conv_desc_t* d, const mlstm::ConvParams& p) {
+    const int64_t size = (int64_t)size_of(d->dtype), B = d->B, S = d->S, D = d->D, K = d->K;
+    rows = B * S * D * size;
+    state = B * (K - 1) * D * size;
+    weight = 4 * D * K;
+    bias = 4 * D;
+    in = {span(p.x, B, S, D, size), span(p.weight, weight), span(p.bias, bias)};
+  }
+};
+
 int validate(const mlstm_scan_desc_t* d) {
   if (!d) return MLSTM_E_NULLPTR;
   if (bad_shape(d->B, d->S, d->D, 0)) return MLSTM_E_SHAPE;
@@ -112,6 +152,23 @@ mlstm::ScanParams params(const mlstm_scan_desc_t* d, const void* x, const void* 
   p.bf16 = d->dtype == MLSTM_BF16;
   return p;
 }
+
+// The inputs' memory but the state's, and the bytes of x's rows, Bm's, the state,
+// A and a value a channel.
+struct ScanSpans {
+  int64_t rows, columns, state, A, channels;
+  std::array<Span, 8> in;
+  ScanSpans(const mlstm_scan_desc_t* d, const mlstm::ScanParams& p) {
+    const int64_t size = (int64_t)size_of(d->dtype), B = d->B, S = d->S, D = d->D, N = d->N;
+    rows = B * S * D * size;
+    columns = B * S * N * size;
+    state = 4 * B * D * N;
+    A = 4 * D * N;
+    channels = 4 * D;
+    in = {span(p.x, B, S, D, size),  span(p.dt, B, S, D, size), span(p.z, B, S, D, size),  span(p.Bm, B, S, N, size),
+          span(p.Cm, B, S, N, size), span(p.A, A),              span(p.Dskip, channels), span(p.bias, channels)};
+  }
+};
 
 // Cuts the sequence, places the workspace (none: sizes only) and returns its bytes.
 size_t place(mlstm::ScanParams& p, bool back, void* workspace) {
@@ -183,6 +240,10 @@ int mlstm_conv_fw(const mlstm_conv_desc_t* desc, const void* x, const float* wei
   mlstm::ConvParams p = params(desc, x, weight, bias, state, false);
   p.y = y;
   p.state_out = state_out;
+  const ConvSpans n(desc, p);
+  const Spans outs = {span(y, n.rows), span(state_out, n.state)};
+  if ((st = check_apart(outs, n.in)) != MLSTM_OK) return st;
+  if ((st = check_apart(outs, Spans{span(state, n.state)})) != MLSTM_OK) return st;
   if (p.S == 0 && !state_out) return MLSTM_OK;
   return status(mlstm::launch_conv(p, static_cast<hipStream_t>(stream)));
 }
@@ -205,6 +266,10 @@ int mlstm_conv_bw(const mlstm_conv_desc_t* desc, const void* x, const float* wei
   p.dweight = dweight;
   p.dbias = dbias;
   p.partial = sums ? static_cast<float*>(workspace) : nullptr;
+  const ConvSpans n(desc, p);
+  const Spans outs = {span(dx, n.rows), span(dstate, n.state), span(dweight, n.weight), span(dbias, n.bias)};
+  if ((st = check_apart(outs, n.in)) != MLSTM_OK) return st;
+  if ((st = check_apart(outs, Spans{span(state, n.state), span(dy, n.rows), span(dstate_out, n.state)})) != MLSTM_OK) return st;
   return status(mlstm::launch_conv_back(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -219,6 +284,11 @@ int mlstm_conv_step(const mlstm_conv_desc_t* desc, const void* x, const float* w
   mlstm::ConvParams p = params(desc, x, weight, bias, state, false);
   p.y = y;
   p.state_out = state_out;
+  const ConvSpans n(desc, p);
+  if ((st = check_apart({span(y, n.rows), span(state_out, n.state)}, n.in)) != MLSTM_OK) return st;
+  if ((st = check_apart({span(y, n.rows), span(state != state_out ? state_out : nullptr, n.state)},
+                        Spans{span(state, n.state)})) != MLSTM_OK)
+    return st;
   return status(mlstm::launch_conv_step(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -240,6 +310,10 @@ int mlstm_scan_fw(const mlstm_scan_desc_t* desc, const void* x, const void* dt, 
   if (!workspace_ok(workspace, workspace_bytes, place(p, false, workspace))) return MLSTM_E_WORKSPACE;
   p.y = y;
   p.h_out = h_out;
+  const ScanSpans n(desc, p);
+  const Spans outs = {span(y, n.rows), span(h_out, n.state)};
+  if ((st = check_apart(outs, n.in)) != MLSTM_OK) return st;
+  if ((st = check_apart(outs, Spans{span(h0, n.state)})) != MLSTM_OK) return st;
   if (p.S == 0 && !h_out) return MLSTM_OK;
   return status(mlstm::launch_scan(p, static_cast<hipStream_t>(stream)));
 }
@@ -270,6 +344,12 @@ int mlstm_scan_bw(const mlstm_scan_desc_t* desc, const void* x, const void* dt, 
   p.dz = dz;
   p.dbias = dbias;
   p.dh0 = dh0;
+  const ScanSpans n(desc, p);
+  const Spans outs = {span(dx, n.rows),        span(ddt, n.rows),       span(dA, n.A),
+                      span(dBm, n.columns),    span(dCm, n.columns),    span(dDskip, n.channels),
+                      span(dz, n.rows),        span(dbias, n.channels), span(dh0, n.state)};
+  if ((st = check_apart(outs, n.in)) != MLSTM_OK) return st;
+  if ((st = check_apart(outs, Spans{span(h0, n.state), span(dy, n.rows), span(dh_out, n.state)})) != MLSTM_OK) return st;
   return status(mlstm::launch_scan_back(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -286,6 +366,11 @@ int mlstm_scan_step(const mlstm_scan_desc_t* desc, const void* x, const void* dt
   mlstm::ScanParams p = params(desc, x, dt, A, Bm, Cm, Dskip, z, dt_bias, h_in);
   p.y = y;
   p.h_out = h_out;
+  const ScanSpans n(desc, p);
+  if ((st = check_apart({span(y, n.rows), span(h_out, n.state)}, n.in)) != MLSTM_OK) return st;
+  if ((st = check_apart({span(y, n.rows), span(h_in != h_out ? h_out : nullptr, n.state)},
+                        Spans{span(h_in, n.state)})) != MLSTM_OK)
+    return st;
   return status(mlstm::launch_scan_step(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -299,6 +384,10 @@ int mlstm_dropout(const mlstm_dropout_desc_t* desc, const void* x, const void* r
   if (any_null({x, y})) return MLSTM_E_NULLPTR;
   if ((st = check_aligned({x, residual, y}, size_of(desc->dtype))) != MLSTM_OK) return st;
   if ((st = check_aligned({seed_dev}, 8)) != MLSTM_OK) return st;
+  const int64_t bytes = desc->n * (int64_t)size_of(desc->dtype);
+  if ((st = check_apart({span(y, bytes)}, Spans{span(x != y ? x : nullptr, bytes), span(residual != y ? residual : nullptr, bytes),
+                                                span(seed_dev, 16)})) != MLSTM_OK)
+    return st;
   mlstm::DropoutParams p = {};
   p.x = x;
   p.residual = residual;
