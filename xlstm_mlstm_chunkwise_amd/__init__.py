@@ -1224,7 +1224,6 @@ def causal_conv_fw(x, weight, bias=None, state=None, *, activation: Optional[str
     front of x, or None (zeros); activation None or "silu".  Returns (y, state'),
     state' None when return_final_state is False.  out shares no memory with an
     input."""
-    torch = _torch()
     dev, B, S, D, K, desc, _ = _conv_inputs("mlstm_conv_fw", x, weight, bias, state, activation)
     if out is not None:
         _check_on(dev, "y", out, (B, S, D), x.dtype)
@@ -1389,7 +1388,6 @@ def selective_scan_fw(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, 
     None when return_final_state is False.  A token with dt = -inf leaves the
     state as it is, so rows of padding need that and finite x and B.  out shares
     no memory with an input."""
-    torch = _torch()
     dev = _gpu_input(x, 3, "(B, S, D)")
     nb, S, ch, N, (desc, need, _) = _scan_inputs("mlstm_scan_fw", dev, x, dt, A, B, C, D, z, dt_bias, h0)
     if out is not None:

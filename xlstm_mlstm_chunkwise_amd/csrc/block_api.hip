@@ -100,7 +100,7 @@ mlstm::ConvParams params(const mlstm_conv_desc_t* d, const void* x, const float*
   p.K = d->K;
   p.bf16 = d->dtype == MLSTM_BF16;
   p.silu = d->silu;
-  mlstm::conv_runs(p.B, p.S, p.D, p.K, back, &p.run, &p.runs);
+  mlstm::conv_runs(p.B, p.S, p.D, back, &p.run, &p.runs);
   return p;
 }
 

@@ -400,7 +400,7 @@ hipError_t launch_types(const ConvParams& p, Pass pass, hipStream_t stream) {
 // 3 of 1777 x 960: forward 8.3 us in runs of 8, 9.2 of 4, 9.4 of 16; backward with
 // its sums 18.9 us in runs of 16, 21.2 of 8, 19.5 of 32; 1 of 256 x 64 forward 4.2
 // in runs of 8, 5.2 of 16.
-void conv_runs(int B, int S, int D, int K, bool back, int* run, int* runs) {
+void conv_runs(int B, int S, int D, bool back, int* run, int* runs) {
   const int64_t lanes = (int64_t)B * ((D + 3) / 4), rows = S;
   const int64_t waves = back ? 4096 : 8192, least = back ? 16 : 8, most = back ? 512 : 64;
   int64_t per = (waves * 64 + lanes - 1) / lanes, len = (rows + per - 1) / per;

@@ -360,7 +360,7 @@ struct ConvParams {
   int bf16, silu;
 };
 // Rows a run has, and runs of all sequences together.
-void conv_runs(int B, int S, int D, int K, bool back, int* run, int* runs);
+void conv_runs(int B, int S, int D, bool back, int* run, int* runs);
 hipError_t launch_conv(const ConvParams& p, hipStream_t stream);
 hipError_t launch_conv_back(const ConvParams& p, hipStream_t stream);
 hipError_t launch_conv_step(const ConvParams& p, hipStream_t stream);
