@@ -753,7 +753,10 @@ int mlstm_conv_step(const mlstm_conv_desc_t* desc,
  *   r_t[c]    = sum_n Cm_t[n] h_t[c, n] + Dskip[c] x_t[c]
  *   y_t[c]    = r_t[c] z_t[c] sigmoid(z_t[c])           (z given; else r_t[c])
  *
- * States, sums and products in float32.  A is finite.  dt = -inf leaves the
+ * States, sums and products in float32.  A is finite, and a channel's decays
+ * multiplied over any run of tokens stay below 2^128, as they always do for A <=
+ * 0: the sequence is walked in pieces, and a product that overflows gives NaN
+ * also for a state or a gradient that is zero.  dt = -inf leaves the
  * state as it is (d = 0) where x and Bm are finite.  A non-finite x, dt, z or dy
  * stays in its channel, from its token on (of the backward pass also in front of
  * it), but for dBm and dCm of the tokens that it reaches there; a non-finite Bm

@@ -142,6 +142,17 @@ def _gpu_draw(B, S, D, N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape,cut", [CUTS[1], CUTS[3], CUTS[6]])
+def test_growing_states(mt, shape, cut):
+    """A of either sign: products of decays up to e^5 and back to e^-5."""
+    assert_cut(mt, *shape, *cut)
+    kw, dy, dh = _draw(sum(shape) + 1, *shape, "f32")
+    steps = np.logaddexp(0, kw["dt"] + kw["dt_bias"]).sum(1).max()
+    kw["A"] = (5 / steps * np.random.default_rng(2).uniform(-1, 1, kw["A"].shape)).astype(np.float32)
+    _check(mt, kw, dy, dh, "f32")
+
+
+@pytest.mark.gpu
 def test_the_walk_is_the_oracles(mt):
     g, dy, dh = _gpu_draw(2, 40, 24, 16)
     kw, host = {k: v.cpu().numpy() for k, v in g.items()}, (dy.cpu().numpy(), dh.cpu().numpy())

@@ -1384,10 +1384,11 @@ def selective_scan_fw(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, 
     x, dt, z (B, S, D) and B, C (B, S, N), all bfloat16 or all float32,
     contiguous or a run of columns of a wider tensor, N 16, 32 or 64, z or None
     (no gate); A (D, N), D and dt_bias (D) or None (zeros), h0 (B, D, N) or None
-    (zero state), float32.  Returns (y, h): y in x's dtype, h (B, D, N) float32,
-    None when return_final_state is False.  A token with dt = -inf leaves the
-    state as it is, so rows of padding need that and finite x and B.  out shares
-    no memory with an input."""
+    (zero state), float32.  A is at most 0, or so small that the decays of a run
+    of tokens multiply to less than 2^128.  Returns (y, h): y in x's dtype, h
+    (B, D, N) float32, None when return_final_state is False.  A token with dt =
+    -inf leaves the state as it is, so rows of padding need that and finite x and
+    B.  out shares no memory with an input."""
     dev = _gpu_input(x, 3, "(B, S, D)")
     nb, S, ch, N, (desc, need, _) = _scan_inputs("mlstm_scan_fw", dev, x, dt, A, B, C, D, z, dt_bias, h0)
     if out is not None:
