@@ -777,8 +777,10 @@ int mlstm_scan_validate(const mlstm_scan_desc_t* desc);
 /* Bytes of device workspace; 0 for an invalid descriptor.  Forward: Bm and Cm
  * in float32 and, where the sequence is cut into chunks that are walked side by
  * side, a state and a float a channel for each.  Backward: also the state in
- * front of every eight tokens and, for every 128 channels, a part of dBm and
- * dCm, all in float32. */
+ * front of every eight tokens; for every 2048 / N channels a part of dBm and
+ * dCm; for every span of tokens (walked side by side too) a part of dA, dDskip
+ * and dbias and, where there are several, the state gradient that it hands on
+ * and a float a channel.  All in float32. */
 size_t mlstm_scan_fw_workspace_bytes(const mlstm_scan_desc_t* desc);
 size_t mlstm_scan_bw_workspace_bytes(const mlstm_scan_desc_t* desc);
 

@@ -378,7 +378,7 @@ hipError_t launch_columns(const ScanParams& p, hipStream_t stream) {
 
 void scan_cut(ScanParams& p, bool back) {
   const int tiles = p.rows / kScanTile;
-  // n pieces of whole tiles, four at least; every one has tokens
+  // at most n pieces of whole tiles, two of them at least; every one has tokens
   auto cut = [&](int64_t n, int* pieces, int* length) {
     if (n > tiles / 2) n = tiles / 2;
     if (n > 64) n = 64;
