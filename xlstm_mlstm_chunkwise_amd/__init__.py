@@ -32,10 +32,11 @@ _SCHED = {"auto": MLSTM_SCHED_AUTO, "two_stage": MLSTM_SCHED_TWO_STAGE, "fused":
 MLSTM_STATES_SPLIT, MLSTM_STATES_I16 = 0, 1
 _CODES = {"split": MLSTM_STATES_SPLIT, "int16": MLSTM_STATES_I16}
 
+MLSTM_E_OVERLAP = 10
 STATUS_NAMES = {
     0: "MLSTM_OK", 1: "MLSTM_E_NULLPTR", 2: "MLSTM_E_SHAPE", 3: "MLSTM_E_CHUNK",
     4: "MLSTM_E_DTYPE", 5: "MLSTM_E_UNSUPPORTED", 6: "MLSTM_E_WORKSPACE",
-    7: "MLSTM_E_HIP", 8: "MLSTM_E_ALIGN", 9: "MLSTM_E_ARG", 10: "MLSTM_E_OVERLAP",
+    7: "MLSTM_E_HIP", 8: "MLSTM_E_ALIGN", 9: "MLSTM_E_ARG", MLSTM_E_OVERLAP: "MLSTM_E_OVERLAP",
 }
 
 
@@ -815,7 +816,7 @@ def _call(where, dev, *args):
         with torch.cuda.device(index):
             st = fn(*args, stream)
     if st:
-        raise (OverlapError if st == 10 else MlstmError)(st, where)
+        raise (OverlapError if st == MLSTM_E_OVERLAP else MlstmError)(st, where)
 
 
 def _bytes_of(need, workspace, dev):
